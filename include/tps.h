@@ -26,8 +26,14 @@
  *   attention        on each shard's own heads between QKV and o_proj: causal GQA
  *                    softmax(Q K^T / sqrt(d)) V per head (section "Attention 里的
  *                    tensor parallel": attention per GPU on its local heads).
+ *   serving          the same attention with a sliding window and a few first tokens
+ *                    that stay visible; KV caches per shard, the attention of one new
+ *                    token per sequence against them, and against a prefix that the
+ *                    batch shares.
  *   greedy lm_head   vocab split column-parallel; each shard's argmax over its vocab
  *                    slice, then the max over shards (section "lm_head 怎么处理").
+ *   sampling         temperature, top-k, top-p and min-p over the same logits, from
+ *                    given uniform numbers (the section names top-k and top-p).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -119,7 +125,8 @@ enum {
 };
 
 /* Function ids for tps_workspace_bytes(). */
-enum { TPS_FN_COLUMN = 0, TPS_FN_ROW = 1, TPS_FN_MLP = 2, TPS_FN_ATTN = 3, TPS_FN_ARGMAX = 4 };
+enum { TPS_FN_COLUMN = 0, TPS_FN_ROW = 1, TPS_FN_MLP = 2, TPS_FN_ATTN = 3, TPS_FN_ARGMAX = 4,
+       TPS_FN_SAMPLE = 5 };
 
 /* Attention head geometry (QKV kind and the attention composite). */
 typedef struct {
@@ -326,6 +333,120 @@ TPS_API int sharded_gqa_attention(const void* qkv, int64_t nseq, int64_t seqlen,
                                   int tp, int causal, void* attn_out, void* stream);
 
 /*
+ * sharded_window_attention -- sharded_gqa_attention (causal) with a sliding window and
+ *   sinks: query t of a sequence sees key j <= t when t - j < window or j < nsink, so
+ *   the last `window` tokens, itself included, and the first nsink. window >= 1 and
+ *   nsink >= 0 of any size (a window of seqlen or more is plain causal attention).
+ *   Layouts, precision and errors as sharded_gqa_attention. Only the key blocks of 128
+ *   that some query of a block sees are read and computed. Every k and v entry of a
+ *   sequence has to be finite: inside a block, a weight of zero times an infinity or a
+ *   NaN of v is a NaN. Other sequences are never read.
+ */
+TPS_API int sharded_window_attention(const void* qkv, int64_t nseq, int64_t seqlen, const tps_heads* heads, int tp,
+                                     int64_t window, int64_t nsink, void* attn_out, void* stream);
+
+/*
+ * KV caches. k_cache, v_cache: device bf16 [nseq][tp*kvs][cap][d], caller-owned, kvs =
+ *   KV heads per shard (tp_head_map), KV head j of shard r at index r*kvs + j (a
+ *   replicated head has a copy per shard, as in a deployment). The first nsink
+ *   positions of a sequence keep the slots 0..nsink-1; position t >= nsink has slot
+ *   nsink + (t - nsink) mod (cap - nsink): a ring, which is a plain linear cache as
+ *   long as no position reaches cap. 0 <= nsink < cap. Slots that no position was
+ *   written to may hold anything. head_dim must be 128.
+ *
+ * sharded_kv_append -- writes the K and V of a QKV output (layout of
+ *   column_parallel_forward, row b*seqlen + i = token i of sequence b) to the caches:
+ *   token i gets position pos[b] + i. pos: device int32 [nseq], the position of token 0,
+ *   or NULL (0 for every sequence); a negative pos[b] appends nothing. count: device
+ *   int32 [nseq], the tokens of sequence b to append (a padded batch; values outside
+ *   [0, seqlen] are clamped), or NULL (seqlen). Where the ring is shorter than the call,
+ *   the newest token of a slot is the one written. Other slots keep their bits.
+ *   Errors: TPS_ERR_ARG, TPS_ERR_DIVISIBILITY, TPS_ERR_UNIMPLEMENTED (head_dim),
+ *   TPS_ERR_ALIGN, TPS_ERR_DEVICE, TPS_ERR_CUDA.
+ */
+TPS_API int sharded_kv_append(const void* qkv, int64_t nseq, int64_t seqlen, const tps_heads* heads, int tp,
+                              const int32_t* pos, const int32_t* count, int64_t nsink, void* k_cache,
+                              void* v_cache, int64_t cap, void* stream);
+
+/*
+ * sharded_window_decode -- one new token per sequence: appends its K and V at position
+ *   pos[b] (as sharded_kv_append) and computes its attention over the cache: position j
+ *   <= pos[b] is seen when pos[b] - j < window or j < nsink. 1 <= window <= cap - nsink,
+ *   so every position of the window is still in the ring; window = cap, nsink = 0 is
+ *   plain decoding from a linear cache. The seen positions have to have been appended
+ *   before. qkv: device bf16 [nseq, tp*(hq/tp + 2*kvs)*d]; attn_out: device bf16
+ *   [nseq, hq*d], the input layout of the o_proj row pack. A row with pos[b] < 0 is an
+ *   unused slot of the batch: its caches stay as they are and its output is zero.
+ *   ws: device workspace of at least tps_decode_workspace_bytes(nseq, heads, tp, 0)
+ *   bytes, zero-filled before its first use and left ready for the next call; calls
+ *   that share one are ordered by their stream. The positions are read on the device:
+ *   a captured graph replays with the positions of its replay.
+ *   Softmax in fp32, weights rounded to bf16 for the product with V (fp32 accumulation).
+ *   Errors as sharded_kv_append, and TPS_ERR_WORKSPACE.
+ */
+TPS_API int sharded_window_decode(const void* qkv, int64_t nseq, const tps_heads* heads, int tp, const int32_t* pos,
+                                  int64_t window, int64_t nsink, void* k_cache, void* v_cache, int64_t cap,
+                                  void* attn_out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * sharded_prefix_decode -- sharded_window_decode for a batch whose sequences share a
+ *   prefix: every new token sees the prefix_len prefix keys and then the positions
+ *   0..pos[b] of its own linear cache (nsink = 0). The prefix is read once for the whole
+ *   batch. prefix_k, prefix_v: device bf16 [tp*kvs][prefix_len][d] (ignored, may be NULL,
+ *   when prefix_len = 0). pos[b] counts the tokens behind the prefix; a row with pos[b]
+ *   outside [0, cap) is unused as above. ws: at least
+ *   tps_decode_workspace_bytes(nseq, heads, tp, prefix_len) bytes.
+ */
+TPS_API int sharded_prefix_decode(const void* qkv, int64_t nseq, const tps_heads* heads, int tp,
+                                  const void* prefix_k, const void* prefix_v, int64_t prefix_len,
+                                  const int32_t* pos, void* k_cache, void* v_cache, int64_t cap, void* attn_out,
+                                  void* ws, size_t ws_bytes, void* stream);
+
+/* tps_decode_workspace_bytes -- workspace of the two decode calls; 0 for invalid arguments. */
+TPS_API size_t tps_decode_workspace_bytes(int64_t nseq, const tps_heads* heads, int tp, int64_t prefix_len);
+
+/*
+ * logits_sample -- draws one token per row of logits [m, V] (logits_dtype BF16 or F32)
+ *   from given uniform numbers. Per row, in this order:
+ *     weights  w_i = exp((l_i - max l) / temperature)
+ *     top_k    keeps the top_k largest logits (equal logits: the lower index first);
+ *              top_k <= 0 or >= V keeps all
+ *     top_p    of what is left, in descending order (equal logits: the lower index
+ *              first), keeps token j when the weight before it is below top_p times the
+ *              sum, the first always; top_p >= 1 keeps all
+ *     min_p    keeps w_i >= min_p, the largest always; min_p <= 0 keeps all
+ *     draw     out_idx = the first kept index, in vocabulary order, whose running sum of
+ *              kept weights exceeds u times their total
+ *     out_logp = log of the drawn token's share of the kept weight
+ *   u, temperature, top_p, min_p: device fp32 [m]; top_k: device int32 [m]; u in [0, 1)
+ *   (values outside are taken as its ends). temperature, top_k, top_p, min_p may be NULL:
+ *   1, all, all, all. temperature <= 0 (or NaN) is greedy: the largest logit, the lowest
+ *   index on ties. Logits of -inf and NaN are never drawn; +inf logits share the weight
+ *   equally; a row without any other logit gives out_idx -1 and out_logp -inf.
+ *   Weights and sums are 64-bit integers in units of 2^-44 of the largest weight, so a
+ *   result depends neither on the order of the additions nor on the launch.
+ *   out_logp: device fp32 [m] or NULL. V must be a multiple of 8 (TPS_ERR_ALIGN) and at
+ *   most 393216 (TPS_ERR_UNIMPLEMENTED). Errors: TPS_ERR_ARG, TPS_ERR_DTYPE,
+ *   TPS_ERR_ALIGN, TPS_ERR_DEVICE, TPS_ERR_CUDA.
+ */
+TPS_API int logits_sample(const void* logits, int logits_dtype, int64_t m, int64_t V, const float* u,
+                          const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                          int32_t* out_idx, float* out_logp, void* stream);
+
+/*
+ * vocab_parallel_sample -- logits_sample over a vocab-parallel lm_head, beside
+ *   vocab_parallel_argmax: logits = X W in fp32 (W[H, V] as a COLUMN pack), then the
+ *   draw over the whole vocabulary. ws: device workspace of at least
+ *   tps_workspace_bytes(TPS_FN_SAMPLE, m, V, H, tp) bytes (required; it holds the
+ *   logits; its status word zero before first use). Other arguments and errors as
+ *   vocab_parallel_argmax and logits_sample.
+ */
+TPS_API int vocab_parallel_sample(const void* X, int64_t m, int64_t H, const void* packed_w, int64_t V, int tp,
+                                  const float* u, const float* temperature, const int32_t* top_k,
+                                  const float* top_p, const float* min_p, int32_t* out_idx, float* out_logp,
+                                  void* ws, size_t ws_bytes, void* stream);
+
+/*
  * row_parallel_forward_noalloc -- row_parallel_forward (FUSED reduction) for
  *   callers that cannot allocate device memory and cannot hand in a workspace:
  *   for example an inference engine that has reserved all device memory up
@@ -355,7 +476,8 @@ TPS_API int row_parallel_forward_noalloc(const void* X, int64_t m, int64_t k, co
  *   COLUMN, 2*I for GATE_UP), TPS_FN_ROW (n = output width, k = input width),
  *   TPS_FN_MLP (n = H, k = I; gated MLP needs the same or less),
  *   TPS_FN_ATTN (n = H, k = hq*d), TPS_FN_ARGMAX (n = V, k = H: the per-tile
- *   maxima of vocab_parallel_argmax, required). Plans given a smaller workspace fall back to
+ *   maxima of vocab_parallel_argmax, required), TPS_FN_SAMPLE (n = V, k = H: the
+ *   logits of vocab_parallel_sample, required). Plans given a smaller workspace fall back to
  *   fewer splits (never to an error). Uses the current device's SM count when a
  *   GPU is present, else 148. Returns 0 for invalid arguments.
  */

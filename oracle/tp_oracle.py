@@ -28,6 +28,7 @@ __all__ = [
     "head_map", "qkv_shard_columns", "qkv_sharded", "qkv_unsharded", "attn_proj_sharded",
     "valid_tp_sizes", "vocab_parallel_argmax", "attention_head", "gqa_attention",
     "gqa_attention_sharded", "row_parallel_bf16_allreduce",
+    "visible_positions", "attend", "window_attention_sharded", "cache_slot", "kv_append", "cached_decode", "sample_row",
 ]
 
 
@@ -425,3 +426,127 @@ def row_parallel_bf16_allreduce(X, V, tp: int, b=None):
     if b is not None:
         Y = bf16_round(Y + to_f64(b)[None, :])
     return Y, Pr
+
+
+# ---------------------------------------------------------------- serving: windows, caches, sampling
+def visible_positions(t: int, window: int, nsink: int):
+    """Positions that the token at position t sees: itself and the window - 1 tokens before
+    it, and the first nsink positions of its sequence."""
+    return [j for j in range(t + 1) if t - j < window or j < nsink]
+
+
+def attend(q, K, V):
+    """softmax(K q / sqrt(d)) V for one query over the keys given, and the same weights over
+    |V| (the size that a rounding of the weights is measured against)."""
+    s = (to_f64(K) @ to_f64(q)) / math.sqrt(len(q))
+    w = np.exp(s - s.max())
+    w = w / w.sum()
+    return w @ to_f64(V), w @ np.abs(to_f64(V))
+
+
+def _local_heads(hq: int, hkv: int, d: int, tp: int):
+    """(query head, first q / k / v column of a shard-major qkv row, KV head slot r*kvs + j)."""
+    q_heads, kv_heads = head_map(hq, hkv, tp)
+    col, out = 0, []
+    for r in range(tp):
+        qs, kvs = len(q_heads[r]), len(kv_heads[r])
+        for j, h in enumerate(q_heads[r]):
+            lk = kv_heads[r].index(h // (hq // hkv))
+            out.append((h, col + j * d, col + (qs + lk) * d, col + (qs + kvs + lk) * d, r * kvs + lk))
+        col += (qs + 2 * kvs) * d
+    return out
+
+
+def window_attention_sharded(qkv, hq: int, hkv: int, d: int, tp: int, nseq: int, S: int, window: int, nsink: int):
+    """Attention on local heads where every query sees visible_positions(). Returns
+    (A [nseq*S, hq*d], the same weights over |V|)."""
+    qkv = to_f64(qkv)
+    out, mag = np.zeros((nseq * S, hq * d)), np.zeros((nseq * S, hq * d))
+    i, j = np.arange(S)[:, None], np.arange(S)[None, :]
+    see = (j <= i) & ((i - j < window) | (j < nsink))
+    for h, qc, kc, vc, _ in _local_heads(hq, hkv, d, tp):
+        for b in range(nseq):
+            x = qkv[b * S:(b + 1) * S]
+            s = np.where(see, (x[:, qc:qc + d] @ x[:, kc:kc + d].T) / math.sqrt(d), -np.inf)
+            w = np.exp(s - s.max(axis=1, keepdims=True))
+            w = w / w.sum(axis=1, keepdims=True)
+            out[b * S:(b + 1) * S, h * d:(h + 1) * d] = w @ x[:, vc:vc + d]
+            mag[b * S:(b + 1) * S, h * d:(h + 1) * d] = w @ np.abs(x[:, vc:vc + d])
+    return out, mag
+
+
+def cache_slot(t: int, nsink: int, cap: int) -> int:
+    """Slot of position t: the first nsink keep theirs, the others share a ring."""
+    return t if t < nsink else nsink + (t - nsink) % (cap - nsink)
+
+
+def kv_append(qkv, hq: int, hkv: int, d: int, tp: int, nseq: int, S: int, pos, count, nsink: int, k_cache, v_cache):
+    """Writes K and V of every token to its slot, token after token; k_cache and v_cache
+    [nseq, tp*kvs, cap, d] are changed in place. pos[b] < 0: nothing of sequence b."""
+    qkv = to_f64(qkv)
+    cap = k_cache.shape[2]
+    for b in range(nseq):
+        if pos[b] < 0:
+            continue
+        for i in range(min(max(int(count[b]), 0), S)):
+            s = cache_slot(int(pos[b]) + i, nsink, cap)
+            for _, _, kc, vc, g in _local_heads(hq, hkv, d, tp):
+                k_cache[b, g, s] = qkv[b * S + i, kc:kc + d]
+                v_cache[b, g, s] = qkv[b * S + i, vc:vc + d]
+
+
+def cached_decode(qkv, hq: int, hkv: int, d: int, tp: int, pos, window: int, nsink: int, k_cache, v_cache,
+                  prefix_k=None, prefix_v=None):
+    """One new token per sequence: appended at pos[b], then its attention over the prefix
+    (if any) and the visible positions of its cache. Returns (A [nseq, hq*d], the same
+    weights over |V|); a row with pos[b] < 0 is zero and appends nothing."""
+    qkv = to_f64(qkv)
+    nseq, cap = len(pos), k_cache.shape[2]
+    kv_append(qkv, hq, hkv, d, tp, nseq, 1, pos, [1] * nseq, nsink, k_cache, v_cache)
+    out, mag = np.zeros((nseq, hq * d)), np.zeros((nseq, hq * d))
+    for b in range(nseq):
+        if pos[b] < 0:
+            continue
+        slots = [cache_slot(j, nsink, cap) for j in visible_positions(int(pos[b]), window, nsink)]
+        for h, qc, _, _, g in _local_heads(hq, hkv, d, tp):
+            K, V = k_cache[b, g, slots], v_cache[b, g, slots]
+            if prefix_k is not None:
+                K, V = np.concatenate([prefix_k[g], K]), np.concatenate([prefix_v[g], V])
+            out[b, h * d:(h + 1) * d], mag[b, h * d:(h + 1) * d] = attend(qkv[b, qc:qc + d], K, V)
+    return out, mag
+
+
+def sample_row(logits, u: float, temperature: float = 1.0, top_k: int = 0, top_p: float = 1.0, min_p: float = 0.0):
+    """One draw from a row of logits, step by step from the definition: the tokens in
+    descending order (equal logits: the lower index first); the top_k first of them; of
+    those the ones with less than top_p of their weight before them (the first always);
+    of those the ones with at least min_p of the largest weight; then the first of the
+    kept ones in vocabulary order whose running sum exceeds u times the total. Returns
+    (index, log of its share), or (-1, -inf) for a row without any logit above -inf."""
+    l = to_f64(logits).copy()
+    l[np.isnan(l)] = -np.inf
+    mx = l.max()
+    if mx == -np.inf:
+        return -1, -np.inf
+    if not temperature > 0:
+        return int(np.argmax(l)), 0.0
+    w = np.where(l == mx, 1.0, 0.0) if mx == np.inf else np.exp((l - mx) / temperature)
+    order = sorted(range(len(l)), key=lambda i: (-l[i], i))
+    if top_k > 0:
+        order = order[:top_k]
+    if top_p < 1:
+        total, before, kept = sum(w[i] for i in order), 0.0, []
+        for i in order:
+            if kept and not before < top_p * total:
+                break
+            kept.append(i)
+            before += w[i]
+        order = kept
+    kept = sorted(i for i in order if w[i] >= min_p or l[i] == mx)
+    total, run = sum(w[i] for i in kept), 0.0
+    for i in kept:
+        run += w[i]
+        if run > u * total:
+            return i, math.log(w[i] / total)
+    i = [i for i in kept if w[i] > 0][-1]
+    return i, math.log(w[i] / total)

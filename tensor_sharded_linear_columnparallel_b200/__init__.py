@@ -38,7 +38,7 @@ KIND_COLUMN, KIND_ROW, KIND_QKV, KIND_GATE_UP = 0, 1, 2, 3
 ACT_NONE, ACT_GELU, ACT_SILU_MUL = 0, 1, 2
 DTYPE_BF16, DTYPE_F32 = 0, 1
 REDUCE_FUSED, REDUCE_PARTIALS, REDUCE_BF16 = 0, 1, 2
-FN_COLUMN, FN_ROW, FN_MLP, FN_ATTN, FN_ARGMAX = 0, 1, 2, 3, 4
+FN_COLUMN, FN_ROW, FN_MLP, FN_ATTN, FN_ARGMAX, FN_SAMPLE = 0, 1, 2, 3, 4, 5
 
 PLAN_AUTO, PLAN_TOKEN_MAJOR, PLAN_WEIGHT_MAJOR = 0, 1, 2
 PLAN_FORCE_SPLITK, PLAN_NO_SPLITK = 16, 32
@@ -54,7 +54,8 @@ EXPORTED = (
     "sharded_attn_proj_forward", "tps_workspace_bytes", "tps_status_string",
     "tps_device_error", "tps_set_plan_override", "tps_debug_wait_timeout",
     "row_parallel_forward_noalloc", "vocab_parallel_argmax", "sharded_gqa_attention", "tps_sync_status",
-    "shard_partial_reduce_bf16",
+    "shard_partial_reduce_bf16", "sharded_window_attention", "sharded_kv_append", "sharded_window_decode",
+    "sharded_prefix_decode", "tps_decode_workspace_bytes", "logits_sample", "vocab_parallel_sample",
 )
 
 
@@ -106,6 +107,13 @@ def _load() -> ctypes.CDLL:
         "row_parallel_forward_noalloc": (I, [P, I64, I64, P, I64, I, P, P, I, P]),
         "vocab_parallel_argmax": (I, [P, I64, I64, P, I64, I, P, P, P, SZ, P]),
         "sharded_gqa_attention": (I, [P, I64, I64, HP, I, I, P, P]),
+        "sharded_window_attention": (I, [P, I64, I64, HP, I, I64, I64, P, P]),
+        "sharded_kv_append": (I, [P, I64, I64, HP, I, P, P, I64, P, P, I64, P]),
+        "sharded_window_decode": (I, [P, I64, HP, I, P, I64, I64, P, P, I64, P, P, SZ, P]),
+        "sharded_prefix_decode": (I, [P, I64, HP, I, P, P, I64, P, P, P, I64, P, P, SZ, P]),
+        "tps_decode_workspace_bytes": (SZ, [I64, HP, I, I64]),
+        "logits_sample": (I, [P, I, I64, I64, P, P, P, P, P, P, P, P]),
+        "vocab_parallel_sample": (I, [P, I64, I64, P, I64, I, P, P, P, P, P, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -391,3 +399,222 @@ def row_parallel_forward_noalloc(X: torch.Tensor, packed_v: torch.Tensor, n: int
     _check(lib.row_parallel_forward_noalloc(_ptr(X), m, k, _ptr(packed_v), n, tp, _ptr(bias), _ptr(out), yd,
                                             _stream(stream)), "row_parallel_forward_noalloc")
     return out
+
+
+# ---------------------------------------------------------------- serving: windows, caches, sampling
+class _On:
+    """The call's device and stream: checks that its tensors share one device, makes that
+    device current for the call, and allocates outputs on the stream that writes them."""
+
+    def __init__(self, stream, *tensors):
+        self.dev = tensors[0].device
+        for t in tensors[1:]:
+            if t is not None and t.device != self.dev:
+                raise ValueError(f"tensors on {self.dev} and {t.device}")
+        self.stream = stream
+
+    def __enter__(self):
+        self.guard = torch.cuda.device(self.dev)
+        self.guard.__enter__()
+        if self.stream is None:
+            self.stream = torch.cuda.current_stream()
+        elif self.stream.device != self.dev:
+            self.guard.__exit__(None, None, None)
+            raise ValueError(f"stream of {self.stream.device}, tensors on {self.dev}")
+        self.on = torch.cuda.stream(self.stream)
+        self.on.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        self.on.__exit__(*exc)
+        self.guard.__exit__(*exc)
+
+
+def _qkv_cols(heads: Heads, tp: int) -> tuple[int, int]:
+    """Columns of a QKV output row and KV head slots tp*kvs (every shard's KV heads)."""
+    _, qc, _, kc = tp_head_map(heads.hq, heads.hkv, tp)
+    return tp * (qc[0] + 2 * kc[0]) * heads.head_dim, tp * kc[0]
+
+
+def _shape(t: torch.Tensor, shape: tuple, what: str) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _caches(k_cache, v_cache, nseq: int, nkv: int, d: int) -> int:
+    _dev(k_cache, "k_cache", torch.bfloat16)
+    _dev(v_cache, "v_cache", torch.bfloat16)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [nseq, tp*kvs, cap, d]")
+    cap = k_cache.shape[2]
+    _shape(k_cache, (nseq, nkv, cap, d), "k_cache")
+    _shape(v_cache, (nseq, nkv, cap, d), "v_cache")
+    return cap
+
+
+def _vec(t, n: int, dtype, what: str):
+    if t is not None:
+        _dev(t, what, dtype)
+        _shape(t, (n,), what)
+    return t
+
+
+def sharded_window_attention(qkv: torch.Tensor, nseq: int, seqlen: int, heads: Heads, tp: int, window: int,
+                             nsink: int = 0, out=None, stream=None):
+    """sharded_gqa_attention (causal) where query t sees the last `window` tokens, itself
+    included, and the first `nsink`. Returns attn_out [nseq*seqlen, hq*d] bf16."""
+    _dev(qkv, "qkv", torch.bfloat16)
+    m = nseq * seqlen
+    _shape(qkv, (m, _qkv_cols(heads, tp)[0]), "qkv")
+    if out is not None:
+        _dev(out, "out", torch.bfloat16)
+        _shape(out, (m, heads.hq * heads.head_dim), "out")
+    with _On(stream, qkv, out) as st:
+        if out is None:
+            out = torch.empty(m, heads.hq * heads.head_dim, dtype=torch.bfloat16, device=qkv.device)
+        _check(lib.sharded_window_attention(_ptr(qkv), nseq, seqlen, _heads_ref(heads), tp, window, nsink, _ptr(out),
+                                            st), "sharded_window_attention")
+    return out
+
+
+def sharded_kv_append(qkv: torch.Tensor, nseq: int, seqlen: int, heads: Heads, tp: int, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, pos=None, count=None, nsink: int = 0, stream=None) -> None:
+    """Writes the K and V of a QKV output to the caches [nseq, tp*kvs, cap, d]: token i of
+    sequence b, i < count[b], at position pos[b] + i (int32 [nseq]; None: 0 and seqlen)."""
+    _dev(qkv, "qkv", torch.bfloat16)
+    cols, nkv = _qkv_cols(heads, tp)
+    _shape(qkv, (nseq * seqlen, cols), "qkv")
+    cap = _caches(k_cache, v_cache, nseq, nkv, heads.head_dim)
+    _vec(pos, nseq, torch.int32, "pos")
+    _vec(count, nseq, torch.int32, "count")
+    with _On(stream, qkv, k_cache, v_cache, pos, count) as st:
+        _check(lib.sharded_kv_append(_ptr(qkv), nseq, seqlen, _heads_ref(heads), tp, _ptr(pos), _ptr(count), nsink,
+                                     _ptr(k_cache), _ptr(v_cache), cap, st), "sharded_kv_append")
+
+
+def tps_decode_workspace_bytes(nseq: int, heads: Heads, tp: int, prefix_len: int = 0) -> int:
+    return lib.tps_decode_workspace_bytes(nseq, _heads_ref(heads), tp, prefix_len)
+
+
+def decode_workspace(nseq: int, heads: Heads, tp: int, prefix_len: int = 0, device=None) -> torch.Tensor:
+    """Zero-filled workspace of the decode calls (tps_decode_workspace_bytes bytes)."""
+    dev = torch.device(device or "cuda")
+    with torch.cuda.device(dev):
+        nbytes = tps_decode_workspace_bytes(nseq, heads, tp, prefix_len)
+    return torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=dev)
+
+
+def sharded_window_decode(qkv: torch.Tensor, heads: Heads, tp: int, pos: torch.Tensor, window: int,
+                          k_cache: torch.Tensor, v_cache: torch.Tensor, ws: torch.Tensor, nsink: int = 0, out=None,
+                          stream=None):
+    """One new token per row of qkv: appends it at position pos[b] (int32 [nseq]; negative:
+    an unused row, output zero) and returns its attention [nseq, hq*d] bf16 over the last
+    `window` positions and the first `nsink`."""
+    _dev(qkv, "qkv", torch.bfloat16)
+    nseq = qkv.shape[0]
+    cols, nkv = _qkv_cols(heads, tp)
+    _shape(qkv, (nseq, cols), "qkv")
+    cap = _caches(k_cache, v_cache, nseq, nkv, heads.head_dim)
+    _vec(_dev(pos, "pos", torch.int32), nseq, torch.int32, "pos")
+    _dev(ws, "ws")
+    if out is not None:
+        _dev(out, "out", torch.bfloat16)
+        _shape(out, (nseq, heads.hq * heads.head_dim), "out")
+    with _On(stream, qkv, k_cache, v_cache, pos, ws, out) as st:
+        if out is None:
+            out = torch.empty(nseq, heads.hq * heads.head_dim, dtype=torch.bfloat16, device=qkv.device)
+        _check(lib.sharded_window_decode(_ptr(qkv), nseq, _heads_ref(heads), tp, _ptr(pos), window, nsink,
+                                         _ptr(k_cache), _ptr(v_cache), cap, _ptr(out), _ptr(ws),
+                                         ws.numel() * ws.element_size(), st), "sharded_window_decode")
+    return out
+
+
+def sharded_prefix_decode(qkv: torch.Tensor, heads: Heads, tp: int, prefix_k, prefix_v, pos: torch.Tensor,
+                          k_cache: torch.Tensor, v_cache: torch.Tensor, ws: torch.Tensor, out=None, stream=None):
+    """One new token per row of qkv, behind a prefix [tp*kvs, prefix_len, d] that all rows
+    share (None: no prefix): appends it at position pos[b] of its own linear cache (a row
+    with pos[b] outside [0, cap) is unused, output zero) and returns its attention
+    [nseq, hq*d] bf16 over the prefix and positions 0..pos[b]."""
+    _dev(qkv, "qkv", torch.bfloat16)
+    nseq = qkv.shape[0]
+    cols, nkv = _qkv_cols(heads, tp)
+    _shape(qkv, (nseq, cols), "qkv")
+    cap = _caches(k_cache, v_cache, nseq, nkv, heads.head_dim)
+    P = 0
+    if prefix_k is not None or prefix_v is not None:
+        _dev(prefix_k, "prefix_k", torch.bfloat16)
+        _dev(prefix_v, "prefix_v", torch.bfloat16)
+        P = prefix_k.shape[1] if prefix_k.dim() == 3 else -1
+        _shape(prefix_k, (nkv, P, heads.head_dim), "prefix_k")
+        _shape(prefix_v, (nkv, P, heads.head_dim), "prefix_v")
+    _vec(_dev(pos, "pos", torch.int32), nseq, torch.int32, "pos")
+    _dev(ws, "ws")
+    if out is not None:
+        _dev(out, "out", torch.bfloat16)
+        _shape(out, (nseq, heads.hq * heads.head_dim), "out")
+    with _On(stream, qkv, k_cache, v_cache, pos, ws, out, prefix_k, prefix_v) as st:
+        if out is None:
+            out = torch.empty(nseq, heads.hq * heads.head_dim, dtype=torch.bfloat16, device=qkv.device)
+        _check(lib.sharded_prefix_decode(_ptr(qkv), nseq, _heads_ref(heads), tp, _ptr(prefix_k), _ptr(prefix_v), P,
+                                         _ptr(pos), _ptr(k_cache), _ptr(v_cache), cap, _ptr(out), _ptr(ws),
+                                         ws.numel() * ws.element_size(), st), "sharded_prefix_decode")
+    return out
+
+
+def _sample_params(m, u, temperature, top_k, top_p, min_p, out_idx, out_logp):
+    _vec(_dev(u, "u", torch.float32), m, torch.float32, "u")
+    _vec(temperature, m, torch.float32, "temperature")
+    _vec(top_k, m, torch.int32, "top_k")
+    _vec(top_p, m, torch.float32, "top_p")
+    _vec(min_p, m, torch.float32, "min_p")
+    _vec(out_idx, m, torch.int32, "out_idx")
+    _vec(out_logp, m, torch.float32, "out_logp")
+    return u, temperature, top_k, top_p, min_p, out_idx, out_logp
+
+
+def logits_sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None,
+                  out_idx=None, out_logp=None, stream=None):
+    """Draws one token per row of logits [m, V] (bf16 or fp32) with the uniform numbers u
+    [m]: temperature, top-k, top-p, min-p (per-row tensors or None), then the inverse of
+    the kept weights' running sum in vocabulary order. Returns (indices int32 [m], log of
+    the drawn tokens' shares fp32 [m])."""
+    _dev(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D")
+    m, V = logits.shape
+    par = _sample_params(m, u, temperature, top_k, top_p, min_p, out_idx, out_logp)
+    with _On(stream, logits, *par) as st:
+        if out_idx is None:
+            out_idx = torch.empty(m, dtype=torch.int32, device=logits.device)
+        if out_logp is None:
+            out_logp = torch.empty(m, dtype=torch.float32, device=logits.device)
+        _check(lib.logits_sample(_ptr(logits), _ydtype(logits.dtype), m, V, _ptr(u), _ptr(temperature), _ptr(top_k),
+                                 _ptr(top_p), _ptr(min_p), _ptr(out_idx), _ptr(out_logp), st), "logits_sample")
+    return out_idx, out_logp
+
+
+def vocab_parallel_sample(X: torch.Tensor, H: int, V: int, tp: int, packed_w: torch.Tensor, u: torch.Tensor,
+                          ws: torch.Tensor | None = None, temperature=None, top_k=None, top_p=None, min_p=None,
+                          out_idx=None, out_logp=None, stream=None):
+    """logits_sample over a vocab-parallel lm_head (COLUMN pack of W[H, V]); ws is a
+    workspace(FN_SAMPLE, m, V, H, tp), which receives the fp32 logits."""
+    _dev(X, "X", torch.bfloat16)
+    _dev(packed_w, "packed_w", torch.bfloat16)
+    m = X.shape[0]
+    _shape(X, (m, H), "X")
+    if packed_w.numel() * 2 < tp_packed_bytes(KIND_COLUMN, H, V, tp):
+        raise ValueError("packed_w is smaller than the COLUMN pack of W[H, V]")
+    if ws is not None:
+        _dev(ws, "ws")
+    par = _sample_params(m, u, temperature, top_k, top_p, min_p, out_idx, out_logp)
+    with _On(stream, X, packed_w, ws, *par) as st:
+        if ws is None:
+            ws = workspace(FN_SAMPLE, m, V, H, tp, device=X.device)
+        if out_idx is None:
+            out_idx = torch.empty(m, dtype=torch.int32, device=X.device)
+        if out_logp is None:
+            out_logp = torch.empty(m, dtype=torch.float32, device=X.device)
+        _check(lib.vocab_parallel_sample(_ptr(X), m, H, _ptr(packed_w), V, tp, _ptr(u), _ptr(temperature),
+                                         _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(out_idx), _ptr(out_logp),
+                                         _ptr(ws), ws.numel() * ws.element_size(), st), "vocab_parallel_sample")
+    return out_idx, out_logp

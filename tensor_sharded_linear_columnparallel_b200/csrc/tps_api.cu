@@ -1123,6 +1123,100 @@ int reduce_common(const float* partials, int tp, int64_t m, int64_t n, const voi
              : TPS_ERR_CUDA;
 }
 
+// ------------------------------------------------------------------ attention on local heads, caches
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+constexpr int kEmpty = 1;   // attention_args: a valid problem without tokens
+
+// Checks and kernel arguments that the prefill attentions share (all but the mask and
+// the work items).
+int attention_args(const void* qkv, int64_t nseq, int64_t seqlen, const tps_heads* heads, int tp, void* attn_out,
+                   tps::AttnArgs* out) {
+  HeadMap hm{};
+  int rc = head_map_calc(heads->hq, heads->hkv, tp, &hm);
+  if (rc) return rc;
+  if (heads->head_dim != tps::kAttnHeadDim) return TPS_ERR_UNIMPLEMENTED;
+  const int64_t m = nseq * seqlen;
+  if (nseq > (1LL << 30) || seqlen > (1LL << 30) || m > (1LL << 30)) return TPS_ERR_ARG;
+  if (m == 0) return kEmpty;
+  if (qkv == nullptr || attn_out == nullptr) return TPS_ERR_ARG;
+  if (!aligned16(qkv) || !aligned16(attn_out)) return TPS_ERR_ALIGN;
+  rc = check_device();
+  if (rc) return rc;
+  const int d = heads->head_dim;
+  tps::AttnArgs a{};
+  a.nseq = static_cast<int>(nseq);
+  a.S = static_cast<int>(seqlen);
+  a.hq = heads->hq;
+  a.qs = hm.qs;
+  a.grp = heads->hq / heads->hkv;
+  a.kvs = hm.kvs;
+  a.kv_first_num = hm.kv_num;
+  a.kv_first_den = hm.kv_den;
+  a.shard_cols = (hm.qs + 2 * hm.kvs) * d;
+  a.nqb = static_cast<int>((seqlen + 127) / 128);
+  a.nkb = a.nqb;
+  a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
+  a.out = attn_out;
+  a.ldo = heads->hq * d;
+  a.timeout_ns = kTimeoutNs;
+  *out = a;
+  return TPS_OK;
+}
+
+// Head map and cache geometry of the cache entry points.
+int cache_geom(const tps_heads* heads, int tp, int64_t nsink, int64_t cap, HeadMap* hm) {
+  if (heads == nullptr) return TPS_ERR_ARG;
+  const int rc = head_map_calc(heads->hq, heads->hkv, tp, hm);
+  if (rc) return rc;
+  if (heads->head_dim != tps::kAttnHeadDim) return TPS_ERR_UNIMPLEMENTED;
+  // a column index of a qkv row has to fit 31 bits
+  if (static_cast<int64_t>(tp) * (hm->qs + 2 * hm->kvs) * heads->head_dim > (1LL << 30)) return TPS_ERR_ARG;
+  // at least one slot behind the sinks
+  if (nsink < 0 || cap < 1 || cap > (1LL << 30) || nsink >= cap) return TPS_ERR_ARG;
+  return TPS_OK;
+}
+
+size_t decode_ws(int64_t nseq, const HeadMap& hm, int tp, int64_t prefix_len, int sms) {
+  (void)nseq, (void)hm, (void)tp, (void)prefix_len, (void)sms;
+  return kHdr;
+}
+
+// One decode step; *a carries the mask and the prefix.
+int run_decode(const void* qkv, int64_t nseq, const tps_heads* heads, const HeadMap& hm, int tp, const int32_t* pos,
+               void* k_cache, void* v_cache, int64_t cap, void* attn_out, void* ws, size_t ws_bytes,
+               tps::DecodeArgs* a, cudaStream_t st) {
+  const int64_t nkv = static_cast<int64_t>(tp) * hm.kvs;
+  if (nseq < 0 || nseq > (1LL << 24) || nseq * nkv > (1LL << 30)) return TPS_ERR_ARG;
+  if (nseq == 0) return TPS_OK;
+  if (qkv == nullptr || pos == nullptr || k_cache == nullptr || v_cache == nullptr || attn_out == nullptr ||
+      ws == nullptr)
+    return TPS_ERR_ARG;
+  if (!aligned16(qkv) || !aligned4(pos) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(attn_out) ||
+      !aligned16(ws))
+    return TPS_ERR_ALIGN;
+  const int sms = num_sms_current();
+  if (ws_bytes < decode_ws(nseq, hm, tp, a->prefix_len, sms)) return TPS_ERR_WORKSPACE;
+  const int rc = check_device();
+  if (rc) return rc;
+  a->qkv = static_cast<const __nv_bfloat16*>(qkv);
+  a->nseq = static_cast<int>(nseq);
+  a->tp = tp;
+  a->qs = hm.qs;
+  a->kvs = hm.kvs;
+  a->nkv = static_cast<int>(nkv);
+  a->shard_cols = (hm.qs + 2 * hm.kvs) * heads->head_dim;
+  a->ld = static_cast<long long>(tp) * a->shard_cols;
+  a->pos = pos;
+  a->cap = static_cast<int>(cap);
+  a->k = static_cast<__nv_bfloat16*>(k_cache);
+  a->v = static_cast<__nv_bfloat16*>(v_cache);
+  a->scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(heads->head_dim)));
+  a->out = static_cast<__nv_bfloat16*>(attn_out);
+  a->ldo = heads->hq * heads->head_dim;
+  return tps::launch_decode(*a, st) == 0 ? TPS_OK : TPS_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1438,49 +1532,175 @@ int sharded_attn_proj_forward(const void* X, const void* attn_out, int64_t m, in
 int sharded_gqa_attention(const void* qkv, int64_t nseq, int64_t seqlen, const tps_heads* heads, int tp,
                           int causal, void* attn_out, void* stream) {
   if (heads == nullptr || nseq < 0 || seqlen < 0 || (causal != 0 && causal != 1)) return TPS_ERR_ARG;
-  HeadMap hm{};
-  int rc = head_map_calc(heads->hq, heads->hkv, tp, &hm);
-  if (rc) return rc;
-  if (heads->head_dim != tps::kAttnHeadDim) return TPS_ERR_UNIMPLEMENTED;
-  const int64_t m = nseq * seqlen;
-  if (nseq > (1LL << 30) || seqlen > (1LL << 30) || m > (1LL << 30)) return TPS_ERR_ARG;
-  if (m == 0) return TPS_OK;
-  if (qkv == nullptr || attn_out == nullptr) return TPS_ERR_ARG;
-  if (!aligned16(qkv) || !aligned16(attn_out)) return TPS_ERR_ALIGN;
-  rc = check_device();
-  if (rc) return rc;
-  const int d = heads->head_dim;
   tps::AttnArgs a{};
-  a.nseq = static_cast<int>(nseq);
-  a.S = static_cast<int>(seqlen);
-  a.hq = heads->hq;
-  a.qs = hm.qs;
-  a.grp = heads->hq / heads->hkv;
-  a.kvs = hm.kvs;
-  a.kv_first_num = hm.kv_num;
-  a.kv_first_den = hm.kv_den;
-  a.shard_cols = (hm.qs + 2 * hm.kvs) * d;
-  a.nqb = static_cast<int>((seqlen + 127) / 128);
-  a.nkb = a.nqb;
+  int rc = attention_args(qkv, nseq, seqlen, heads, tp, attn_out, &a);
+  if (rc) return rc == kEmpty ? TPS_OK : rc;
   // plan-override bit 27: one query block per work item instead of two
   const int two_tiles = (g_plan_override.load() & (1 << 27)) ? 0 : 1;
   const int64_t items = nseq * static_cast<int64_t>(heads->hq) * (two_tiles ? (a.nqb + 1) / 2 : a.nqb);
   if (items > (1LL << 30)) return TPS_ERR_ARG;
   a.items = static_cast<int>(items);
   a.causal = causal;
-  a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
-  a.out = attn_out;
-  a.ldo = heads->hq * d;
-  a.timeout_ns = kTimeoutNs;
-  const int64_t cols = static_cast<int64_t>(tp) * a.shard_cols;
+  const uint64_t cols = static_cast<uint64_t>(tp) * a.shard_cols;
+  const uint64_t m = static_cast<uint64_t>(nseq) * static_cast<uint64_t>(seqlen);
   CUtensorMap tm;
-  rc = make_map(&tm, qkv, static_cast<uint64_t>(cols), static_cast<uint64_t>(m), 1, static_cast<uint64_t>(cols) * 2,
-                static_cast<uint64_t>(cols) * 2 * static_cast<uint64_t>(m), 128, 1);
+  rc = make_map(&tm, qkv, cols, m, 1, cols * 2, cols * 2 * m, 128, 1);
   if (rc) return rc;
   const int sms = num_sms_current();
   const int grid = a.items < sms ? a.items : sms;
   return tps::launch_attention(tm, a, two_tiles, grid, static_cast<cudaStream_t>(stream)) == 0 ? TPS_OK
                                                                                                 : TPS_ERR_CUDA;
+}
+
+int sharded_window_attention(const void* qkv, int64_t nseq, int64_t seqlen, const tps_heads* heads, int tp,
+                             int64_t window, int64_t nsink, void* attn_out, void* stream) {
+  if (heads == nullptr || nseq < 0 || seqlen < 0 || window < 1 || nsink < 0) return TPS_ERR_ARG;
+  tps::AttnArgs a{};
+  int rc = attention_args(qkv, nseq, seqlen, heads, tp, attn_out, &a);
+  if (rc) return rc == kEmpty ? TPS_OK : rc;
+  const int64_t items = nseq * static_cast<int64_t>(heads->hq) * ((a.nqb + 1) / 2);
+  if (items > (1LL << 30)) return TPS_ERR_ARG;
+  a.items = static_cast<int>(items);
+  a.causal = 1;
+  a.window = static_cast<int>(std::min(window, seqlen));
+  a.nsink = static_cast<int>(std::min(nsink, seqlen));
+  const uint64_t cols = static_cast<uint64_t>(tp) * a.shard_cols;
+  const uint64_t S = static_cast<uint64_t>(seqlen);
+  CUtensorMap tm;
+  rc = make_map(&tm, qkv, cols, S, static_cast<uint64_t>(nseq), cols * 2, cols * 2 * S, 128, 1);
+  if (rc) return rc;
+  const int sms = num_sms_current();
+  const int grid = a.items < sms ? a.items : sms;
+  return tps::launch_window_attention(tm, a, grid, static_cast<cudaStream_t>(stream)) == 0 ? TPS_OK : TPS_ERR_CUDA;
+}
+
+int sharded_kv_append(const void* qkv, int64_t nseq, int64_t seqlen, const tps_heads* heads, int tp,
+                      const int32_t* pos, const int32_t* count, int64_t nsink, void* k_cache, void* v_cache,
+                      int64_t cap, void* stream) {
+  if (nseq < 0 || seqlen < 0) return TPS_ERR_ARG;
+  HeadMap hm{};
+  int rc = cache_geom(heads, tp, nsink, cap, &hm);
+  if (rc) return rc;
+  if (nseq > (1LL << 30) || seqlen > (1LL << 30) || nseq * seqlen > (1LL << 30)) return TPS_ERR_ARG;
+  // one block of 256 threads copies 16 rows of 256 bytes: the grid has to fit 31 bits
+  const int64_t nkv = static_cast<int64_t>(tp) * hm.kvs;
+  if (nseq * seqlen > (1LL << 34) / nkv) return TPS_ERR_ARG;
+  if (nseq * seqlen == 0) return TPS_OK;
+  if (qkv == nullptr || k_cache == nullptr || v_cache == nullptr) return TPS_ERR_ARG;
+  if (!aligned16(qkv) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(pos) || !aligned4(count))
+    return TPS_ERR_ALIGN;
+  rc = check_device();
+  if (rc) return rc;
+  tps::KvAppendArgs a{};
+  a.qkv = static_cast<const __nv_bfloat16*>(qkv);
+  a.nseq = static_cast<int>(nseq);
+  a.S = static_cast<int>(seqlen);
+  a.tp = tp;
+  a.qs = hm.qs;
+  a.kvs = hm.kvs;
+  a.shard_cols = (hm.qs + 2 * hm.kvs) * heads->head_dim;
+  a.ld = static_cast<long long>(tp) * a.shard_cols;
+  a.pos = pos;
+  a.count = count;
+  a.nsink = static_cast<int>(nsink);
+  a.cap = static_cast<int>(cap);
+  a.k = static_cast<__nv_bfloat16*>(k_cache);
+  a.v = static_cast<__nv_bfloat16*>(v_cache);
+  return tps::launch_kv_append(a, static_cast<cudaStream_t>(stream)) == 0 ? TPS_OK : TPS_ERR_CUDA;
+}
+
+size_t tps_decode_workspace_bytes(int64_t nseq, const tps_heads* heads, int tp, int64_t prefix_len) {
+  HeadMap hm{};
+  if (nseq < 0 || nseq > (1LL << 24) || prefix_len < 0 || prefix_len > (1LL << 30) ||
+      cache_geom(heads, tp, 0, 1, &hm) != TPS_OK)
+    return 0;
+  return decode_ws(nseq, hm, tp, prefix_len, num_sms_current());
+}
+
+int sharded_window_decode(const void* qkv, int64_t nseq, const tps_heads* heads, int tp, const int32_t* pos,
+                          int64_t window, int64_t nsink, void* k_cache, void* v_cache, int64_t cap, void* attn_out,
+                          void* ws, size_t ws_bytes, void* stream) {
+  if (window < 1) return TPS_ERR_ARG;
+  HeadMap hm{};
+  const int rc = cache_geom(heads, tp, nsink, cap, &hm);
+  if (rc) return rc;
+  if (window > cap - nsink) return TPS_ERR_ARG;
+  tps::DecodeArgs a{};
+  a.window = static_cast<int>(window);
+  a.nsink = static_cast<int>(nsink);
+  return run_decode(qkv, nseq, heads, hm, tp, pos, k_cache, v_cache, cap, attn_out, ws, ws_bytes, &a,
+                    static_cast<cudaStream_t>(stream));
+}
+
+int sharded_prefix_decode(const void* qkv, int64_t nseq, const tps_heads* heads, int tp, const void* prefix_k,
+                          const void* prefix_v, int64_t prefix_len, const int32_t* pos, void* k_cache, void* v_cache,
+                          int64_t cap, void* attn_out, void* ws, size_t ws_bytes, void* stream) {
+  if (prefix_len < 0 || prefix_len > (1LL << 30)) return TPS_ERR_ARG;
+  HeadMap hm{};
+  const int rc = cache_geom(heads, tp, 0, cap, &hm);
+  if (rc) return rc;
+  if (nseq > 0 && prefix_len > 0 && (prefix_k == nullptr || prefix_v == nullptr)) return TPS_ERR_ARG;
+  if (prefix_len > 0 && (!aligned16(prefix_k) || !aligned16(prefix_v))) return TPS_ERR_ALIGN;
+  tps::DecodeArgs a{};
+  a.window = static_cast<int>(cap);
+  a.linear = 1;
+  a.pk = static_cast<const __nv_bfloat16*>(prefix_k);
+  a.pv = static_cast<const __nv_bfloat16*>(prefix_v);
+  a.prefix_len = static_cast<int>(prefix_len);
+  return run_decode(qkv, nseq, heads, hm, tp, pos, k_cache, v_cache, cap, attn_out, ws, ws_bytes, &a,
+                    static_cast<cudaStream_t>(stream));
+}
+
+int logits_sample(const void* logits, int logits_dtype, int64_t m, int64_t V, const float* u,
+                  const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                  int32_t* out_idx, float* out_logp, void* stream) {
+  if (m < 0 || m > (1LL << 30) || V <= 0) return TPS_ERR_ARG;
+  if (!valid_dtype(logits_dtype)) return TPS_ERR_DTYPE;
+  if (V % 8) return TPS_ERR_ALIGN;
+  if (V > tps::kSampleMaxVocab) return TPS_ERR_UNIMPLEMENTED;
+  if (m == 0) return TPS_OK;
+  if (logits == nullptr || u == nullptr || out_idx == nullptr) return TPS_ERR_ARG;
+  if (!aligned16(logits) || !aligned4(u) || !aligned4(temperature) || !aligned4(top_k) || !aligned4(top_p) ||
+      !aligned4(min_p) || !aligned4(out_idx) || !aligned4(out_logp))
+    return TPS_ERR_ALIGN;
+  const int rc = check_device();
+  if (rc) return rc;
+  tps::SampleArgs a{};
+  a.logits = logits;
+  a.f32 = logits_dtype == TPS_DTYPE_F32;
+  a.m = static_cast<int>(m);
+  a.V = static_cast<int>(V);
+  a.u = u;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.out_idx = out_idx;
+  a.out_logp = out_logp;
+  return tps::launch_sample(a, static_cast<cudaStream_t>(stream)) == 0 ? TPS_OK : TPS_ERR_CUDA;
+}
+
+int vocab_parallel_sample(const void* X, int64_t m, int64_t H, const void* packed_w, int64_t V, int tp,
+                          const float* u, const float* temperature, const int32_t* top_k, const float* top_p,
+                          const float* min_p, int32_t* out_idx, float* out_logp, void* ws, size_t ws_bytes,
+                          void* stream) {
+  if (m < 0 || m > (1LL << 30)) return TPS_ERR_ARG;
+  PackGeom g{};
+  int rc = pack_geom(TPS_KIND_COLUMN, H, V, tp, nullptr, &g);
+  if (rc) return rc;
+  if (V > tps::kSampleMaxVocab) return TPS_ERR_UNIMPLEMENTED;
+  if (m == 0) return TPS_OK;
+  if (X == nullptr || packed_w == nullptr || u == nullptr || out_idx == nullptr || ws == nullptr) return TPS_ERR_ARG;
+  if (!aligned16(X) || !aligned16(packed_w) || !aligned16(ws) || !aligned4(u) || !aligned4(temperature) ||
+      !aligned4(top_k) || !aligned4(top_p) || !aligned4(min_p) || !aligned4(out_idx) || !aligned4(out_logp))
+    return TPS_ERR_ALIGN;
+  if (ws_bytes < kHdr + static_cast<size_t>(m) * V * 4) return TPS_ERR_WORKSPACE;
+  // the GEMM is given the header alone: whole tiles, its status word in ws
+  float* logits = reinterpret_cast<float*>(static_cast<char*>(ws) + kHdr);
+  rc = column_parallel_forward(X, m, H, packed_w, TPS_KIND_COLUMN, V, tp, nullptr, nullptr, TPS_ACT_NONE, logits,
+                               TPS_DTYPE_F32, ws, kHdr, stream);
+  if (rc) return rc;
+  return logits_sample(logits, TPS_DTYPE_F32, m, V, u, temperature, top_k, top_p, min_p, out_idx, out_logp, stream);
 }
 
 int row_parallel_forward_noalloc(const void* X, int64_t m, int64_t k, const void* packed_v, int64_t n, int tp,
@@ -1527,6 +1747,7 @@ size_t tps_workspace_bytes(int fn, int64_t m, int64_t n, int64_t k, int tp) {
   if (m < 0 || n <= 0 || k <= 0 || tp <= 0) return 0;
   if (fn == TPS_FN_ARGMAX)
     return kHdr + round256(static_cast<size_t>(m) * tp * argmax_entries_bound((n + tp - 1) / tp) * 8);
+  if (fn == TPS_FN_SAMPLE) return kHdr + round256(static_cast<size_t>(m) * static_cast<size_t>(n) * 4);
   if (fn < TPS_FN_COLUMN || fn > TPS_FN_ATTN) return 0;
   return ws_bound(m, n, k, tp, num_sms_current());
 }

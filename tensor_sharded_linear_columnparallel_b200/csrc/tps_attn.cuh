@@ -521,6 +521,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // With a causal mask tile A sees one key block less than tile B (its last block is
 // B's diagonal) and skips it; when the query blocks are odd in number the last item
 // has tile A only.
+//
+// WINDOW: query t sees key j <= t when t - j < window or j < nsink. An item streams only
+// the key blocks that one of its rows sees: the blocks of the sinks and the blocks
+// [w0, last] of the windows, where w0 is tile A's first; tile B's window starts one block
+// later. The order w0, sinks, w0 + 1, ..., last keeps the blocks of either tile
+// contiguous in the stream (A all but the last, B all but the first), which is all that
+// the pipeline above needs. When the sinks reach the windows the item streams 0..last.
+// The tensor map then has the sequence as its third dimension, so the keys behind a
+// sequence's end read as zeros instead of the next sequence's tokens.
 constexpr int kAttn2Stages = 2;                                        // K and V ring stages
 constexpr int kAttnPolyEvery = 4;                                      // exp2 pairs per FMA-polynomial pair
 constexpr int kAttn2Threads = (2 + kAttnSoftWarps) * 32;               // loads, MMA, 2 x 4 softmax warps
@@ -540,10 +549,18 @@ struct AttnPair {
   int seq, h, qa;          // query tiles A = block qa, B = block qa + 1
   int nA, nB, nblk;        // key blocks of tile A, of tile B (0: no tile B), of the item
   int qcol, kcol, vcol;
+  int fB;                  // WINDOW: first streamed block of tile B (0 or 1)
+  int w0, ins;             // WINDOW: first window block; sink blocks streamed after it
 };
+
+// WINDOW: key block of streamed block j.
+__device__ __forceinline__ int attn_window_block(const AttnPair& t, int j) {
+  return j == 0 ? t.w0 : (j <= t.ins ? j - 1 : t.w0 + j - t.ins);
+}
 
 // Items are numbered heaviest first: band 0 holds the last pair of query blocks of
 // every (sequence, head).
+template <bool WINDOW>
 __device__ __forceinline__ AttnPair attn_pair(const AttnArgs& a, int item) {
   AttnPair t;
   const int npairs = (a.nqb + 1) >> 1;
@@ -557,6 +574,19 @@ __device__ __forceinline__ AttnPair attn_pair(const AttnArgs& a, int item) {
   t.nA = a.causal ? t.qa + 1 : a.nkb;
   t.nB = has_b ? (a.causal ? t.qa + 2 : a.nkb) : 0;
   t.nblk = t.nA > t.nB ? t.nA : t.nB;
+  t.fB = t.w0 = t.ins = 0;
+  if constexpr (WINDOW) {
+    const int lo = t.qa * kAttnBlk - a.window + 1;      // first key that tile A's first row sees
+    const int nsb = (a.nsink + kAttnBlk - 1) / kAttnBlk;
+    if (lo > 0 && lo / kAttnBlk > nsb) {
+      t.w0 = lo / kAttnBlk;
+      t.ins = nsb;
+      t.fB = 1;
+      t.nblk += nsb - t.w0;
+      t.nA += nsb - t.w0;
+      if (has_b) t.nB += nsb - t.w0;
+    }
+  }
   attn_head_cols(a, t.h, t.qcol, t.kcol, t.vcol);
   return t;
 }
@@ -598,6 +628,13 @@ __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&w)[8]
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Bits i < n of the 32 bits that start at bit `at` of a row of 128.
+__device__ __forceinline__ uint32_t bits_below(int n, int at) {
+  const int k = n - at;
+  return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u);
+}
+
+template <bool WINDOW>
 __global__ void __launch_bounds__(kAttn2Threads, 1)
     tps_attn2_kernel(const __grid_constant__ CUtensorMap tmQKV, const AttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -668,15 +705,16 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
       bool ok = true;
       griddep_wait();
       for (int item = attn_item_of(0); ok && item < a.items; ++it, item = attn_item_of(it)) {
-        const AttnPair t = attn_pair(a, item);
-        const int row0 = t.seq * a.S;
+        const AttnPair t = attn_pair<WINDOW>(a, item);
+        const int row0 = WINDOW ? 0 : t.seq * a.S;
+        const int seq = WINDOW ? t.seq : 0;
         if (!mbar_wait(q_empty, static_cast<uint32_t>(it & 1) ^ 1u, abort_flag, tmo, a.status)) { ok = false; break; }
         const int ntiles = t.nB > 0 ? 2 : 1;
         mbar_arrive_expect_tx(q_full, ntiles * kAttnTileBytes);
         for (int x = 0; x < ntiles; ++x) {
           const int r = row0 + (t.qa + x) * kAttnBlk;
-          tma_load_3d(sQ + x * kAttnTileBytes, &tmQKV, q_full, t.qcol, r, 0);
-          tma_load_3d(sQ + x * kAttnTileBytes + kAttnHalf, &tmQKV, q_full, t.qcol + 64, r, 0);
+          tma_load_3d(sQ + x * kAttnTileBytes, &tmQKV, q_full, t.qcol, r, seq);
+          tma_load_3d(sQ + x * kAttnTileBytes + kAttnHalf, &tmQKV, q_full, t.qcol + 64, r, seq);
         }
         ++nq;
         for (int j = 0; ok && j < t.nblk; ++j, ++n) {
@@ -690,8 +728,9 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
             const uint32_t dst = (kv ? sV : sK) + st * kAttnTileBytes;
             const int col = kv ? t.vcol : t.kcol;
             mbar_arrive_expect_tx(ful, kAttnTileBytes);
-            tma_load_3d(dst, &tmQKV, ful, col, row0 + j * kAttnBlk, 0);
-            tma_load_3d(dst + kAttnHalf, &tmQKV, ful, col + 64, row0 + j * kAttnBlk, 0);
+            const int kb = WINDOW ? attn_window_block(t, j) : j;
+            tma_load_3d(dst, &tmQKV, ful, col, row0 + kb * kAttnBlk, seq);
+            tma_load_3d(dst + kAttnHalf, &tmQKV, ful, col + 64, row0 + kb * kAttnBlk, seq);
           }
           if (!ok) {   // K of this block may be in flight: count the block
             ++n;
@@ -733,13 +772,14 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
         umma_commit(s_full(x));
       };
       for (int item = attn_item_of(0); ok && item < a.items; ++it, item = attn_item_of(it)) {
-        const AttnPair t = attn_pair(a, item);
-        const int nx[2] = {t.nA, t.nB};
+        const AttnPair t = attn_pair<WINDOW>(a, item);
+        const int nx[2] = {t.nA, t.nB};               // streamed blocks [fx, nx) of each tile
+        const int fx[2] = {0, WINDOW ? t.fB : 0};
         if (!mbar_wait(q_full, static_cast<uint32_t>(it & 1), abort_flag, tmo, a.status)) { ok = false; break; }
         if (!mbar_wait(k_full(slot(0)), sph(0), abort_flag, tmo, a.status)) { ok = false; break; }
         tc_fence_after();
         if (t.nA > 0) issue_s(0, 0);
-        if (t.nB > 0) issue_s(1, 0);
+        if (t.nB > 0 && fx[1] == 0) issue_s(1, 0);
         umma_commit(k_empty(slot(0)));
         if (t.nblk == 1) umma_commit(q_empty);
         any = true;
@@ -748,27 +788,29 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (j >= nx[x]) continue;
-            // the first product of an item overwrites O_X: the previous item's O_X must be read out
-            if (j == 0 && its[x] > 0 &&
-                !mbar_wait(o_free(x), static_cast<uint32_t>((its[x] - 1) & 1), abort_flag, tmo, a.status)) {
-              ok = false;
-              break;
-            }
-            if (!mbar_wait(p_full(x), static_cast<uint32_t>((cnt[x] + j) & 1), abort_flag, tmo, a.status) ||
-                !mbar_wait(v_full(slot(j)), sph(j), abort_flag, tmo, a.status)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            // O_X += P_X(j) V_j: A = P from the first 64 columns of S buffer x (16 keys, 8
-            // columns per MMA), B = V read MN-major from its TMA tile (2048 B = 16 keys)
-            const uint32_t vb = sV + slot(j) * kAttnTileBytes;
+            if (!WINDOW || j >= fx[x]) {
+              // the first product of an item overwrites O_X: the previous item's O_X must be read out
+              if (j == fx[x] && its[x] > 0 &&
+                  !mbar_wait(o_free(x), static_cast<uint32_t>((its[x] - 1) & 1), abort_flag, tmo, a.status)) {
+                ok = false;
+                break;
+              }
+              if (!mbar_wait(p_full(x), static_cast<uint32_t>((cnt[x] + j - fx[x]) & 1), abort_flag, tmo, a.status) ||
+                  !mbar_wait(v_full(slot(j)), sph(j), abort_flag, tmo, a.status)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              // O_X += P_X(j) V_j: A = P from the first 64 columns of S buffer x (16 keys, 8
+              // columns per MMA), B = V read MN-major from its TMA tile (2048 B = 16 keys)
+              const uint32_t vb = sV + slot(j) * kAttnTileBytes;
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_bf16_tmem_a(tmem_base + 256 + x * 128, tmem_base + x * 128 + kk * 8,
-                               smem_desc_sw128_mn(vb + kk * 2048, kAttnHalf), kAttnIdescPV,
-                               (j > 0 || kk > 0) ? 1u : 0u);
-            if (j == nx[x] - 1) umma_commit(o_ready(x));
+              for (int kk = 0; kk < 8; ++kk)
+                umma_bf16_tmem_a(tmem_base + 256 + x * 128, tmem_base + x * 128 + kk * 8,
+                                 smem_desc_sw128_mn(vb + kk * 2048, kAttnHalf), kAttnIdescPV,
+                                 (j > fx[x] || kk > 0) ? 1u : 0u);
+              if (j == nx[x] - 1) umma_commit(o_ready(x));
+            }
             if (j + 1 < nx[x]) {
               if (!k_next) {
                 if (!mbar_wait(k_full(slot(j + 1)), sph(j + 1), abort_flag, tmo, a.status)) { ok = false; break; }
@@ -789,8 +831,10 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
         n += t.nblk;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          cnt[x] += nx[x];
-          if (nx[x] > 0) ++its[x];
+          if (nx[x] > 0) {
+            cnt[x] += nx[x] - fx[x];
+            ++its[x];
+          }
         }
       }
       // every issued MMA must be complete before tensor memory is released
@@ -818,24 +862,40 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
     int it = 0;
     bool ok = true;
     for (int item = attn_item_of(0); ok && item < a.items; ++it, item = attn_item_of(it)) {
-      const AttnPair t = attn_pair(a, item);
+      const AttnPair t = attn_pair<WINDOW>(a, item);
       const int nb = x ? t.nB : t.nA;
       if (nb == 0) continue;                      // no tile B in this item
+      const int fb = (WINDOW && x) ? t.fB : 0;    // streamed blocks [fb, nb)
       const int qblk = t.qa + x;
       const int qidx = qblk * kAttnBlk + row;     // query position within the sequence
       const int lastq = a.causal ? min(qidx, a.S - 1) : a.S - 1;
       float m_ref = -INFINITY;                    // reference max behind P (score units)
       float l_run = 0.f;                          // row sum of the weights against m_ref
-      for (int j = 0; j < nb; ++j) {
-        if (!__all_sync(0xffffffffu, mbar_wait(s_full(x), static_cast<uint32_t>((cnt + j) & 1), abort_flag, tmo,
+      for (int j = fb; j < nb; ++j) {
+        if (!__all_sync(0xffffffffu, mbar_wait(s_full(x), static_cast<uint32_t>((cnt + j - fb) & 1), abort_flag, tmo,
                                                a.status))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int kbase = j * kAttnBlk;
-        const bool masked = (kbase + kAttnBlk > a.S) || (a.causal && j == qblk);
+        const int kb = WINDOW ? attn_window_block(t, j) : j;
+        const int kbase = kb * kAttnBlk;
+        bool masked = (kbase + kAttnBlk > a.S) || (a.causal && kb == qblk);
         const int last = lastq - kbase;           // last visible key of the block
+        [[maybe_unused]] uint32_t vis[4];         // WINDOW: the row's visible keys of a masked block
+        if constexpr (WINDOW) {
+          // the window of the tile's last row starts behind the block's first key, and not every key is a sink
+          masked = masked || (qblk * kAttnBlk + kAttnBlk - a.window > kbase && a.nsink < kbase + kAttnBlk);
+          if (masked)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              vis[k] = bits_below(last + 1, 32 * k) &
+                       (~bits_below(last + 1 - a.window, 32 * k) | bits_below(a.nsink - kbase, 32 * k));
+        }
+        auto hidden = [&](int i) -> bool {
+          if constexpr (WINDOW) return !(vis[i >> 5] & (1u << (i & 31)));
+          else return i > last;
+        };
         // pass 1: the block's row max
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four independent max chains
         {
@@ -844,7 +904,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
           if (masked) {
 #pragma unroll
             for (int i = 0; i < 128; ++i)
-              if (i > last) sv[i] = -INFINITY;
+              if (hidden(i)) sv[i] = -INFINITY;
           }
 #pragma unroll
           for (int i = 0; i < 128; i += 2) m4[(i >> 1) & 3] = fmax3(m4[(i >> 1) & 3], sv[i], sv[i + 1]);
@@ -852,9 +912,9 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         float alpha = 1.f;
         bool rescale = false;
-        if (j == 0 || (mx - m_ref) * c > 8.0f) {
+        if (j == fb || (mx - m_ref) * c > 8.0f) {
           const float m_new = fmaxf(m_ref, mx);
-          if (j > 0) {
+          if (j > fb) {
             alpha = ex2_approx((m_ref - m_new) * c);
             rescale = true;
           }
@@ -883,7 +943,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
           if (masked) {
 #pragma unroll
             for (int i = 0; i < 64; ++i)
-              if (hh * 64 + i > last) sv[i] = -INFINITY;
+              if (hidden(hh * 64 + i)) sv[i] = -INFINITY;
           }
 #pragma unroll
           for (int cc = 0; cc < 4; ++cc) {
@@ -938,7 +998,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free(x));     // the next item's first product may overwrite O_X
-      cnt += nb;
+      cnt += nb - fb;
       ++its;
     }
     tc_fence_before();

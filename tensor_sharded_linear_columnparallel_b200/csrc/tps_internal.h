@@ -4,6 +4,7 @@
 
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 namespace tps {
@@ -92,11 +93,54 @@ struct AttnArgs {
   int nqb, nkb;                    // 128-row query blocks and key blocks per sequence
   int items;                       // work items (see launch_attention)
   int causal;
+  int window, nsink;               // WINDOW kernels: query t sees key j <= t when t - j < window or j < nsink
   float scale_log2;                // log2(e) / sqrt(d)
   void* out;                       // bf16 [nseq*S][ldo]
   int ldo;                         // hq * d
   unsigned long long timeout_ns;
   int* status;                     // launch status word, or null (device-wide word only)
+};
+
+// One append of a QKV output's K and V to the shards' caches (tps_cache.cuh).
+struct KvAppendArgs {
+  const __nv_bfloat16* qkv;        // [nseq*S][ld]
+  long long ld;                    // tp * shard_cols
+  int nseq, S, tp, qs, kvs, shard_cols;
+  const int* pos;                  // [nseq] position of token 0, or null (0); negative: nothing to append
+  const int* count;                // [nseq] tokens to append, or null (S)
+  int nsink, cap;
+  __nv_bfloat16 *k, *v;            // [nseq][tp*kvs][cap][128]
+};
+
+// One decode step against the caches: append at pos[b], then attend to the visible slots
+// (and to the shared prefix, when prefix_len > 0).
+struct DecodeArgs {
+  const __nv_bfloat16* qkv;        // [nseq][ld]
+  long long ld;
+  int nseq, tp, qs, kvs, nkv, shard_cols;
+  const int* pos;                  // [nseq] position of the new token; negative (or, linear, >= cap): row idle
+  int linear;                      // 1: position p is slot p, and pos >= cap is idle
+  int window, nsink, cap;
+  __nv_bfloat16 *k, *v;
+  const __nv_bfloat16 *pk, *pv;    // [nkv][prefix_len][128]
+  int prefix_len;
+  float scale_log2;
+  __nv_bfloat16* out;              // [nseq][ldo]
+  int ldo;
+};
+
+// One sampling launch (tps_sample.cuh). The largest vocabulary is what eight CTAs hold in
+// shared memory as fp32.
+constexpr long long kSampleMaxVocab = 8 * 49152;
+struct SampleArgs {
+  const void* logits;              // [m][V]
+  int f32;                         // fp32 logits, else bf16
+  int m, V;
+  const float* u;
+  const float *temperature, *top_p, *min_p;   // [m] or null
+  const int* top_k;                // [m] or null
+  int* out_idx;
+  float* out_logp;                 // [m] or null
 };
 
 struct PackHost {
@@ -161,6 +205,12 @@ int launch_pack(const PackHost& h, cudaStream_t st);
 // two_tiles = 1: two 128-query blocks per work item sharing their K/V stream
 // (items = nseq * hq * ceil(nqb / 2)); 0: one block per item (items = nseq * hq * nqb).
 int launch_attention(const CUtensorMap& tqkv, const AttnArgs& a, int two_tiles, int grid, cudaStream_t st);
+// The two-tile form with a window and sinks (a.window, a.nsink); the map has the
+// sequence as its third dimension.
+int launch_window_attention(const CUtensorMap& tqkv, const AttnArgs& a, int grid, cudaStream_t st);
+int launch_kv_append(const KvAppendArgs& a, cudaStream_t st);
+int launch_decode(const DecodeArgs& a, cudaStream_t st);
+int launch_sample(const SampleArgs& a, cudaStream_t st);
 int attention_smem_bytes(int two_tiles);
 // bf16_chain = 0: Y = P_0 + ... + P_{tp-1} (+ bias) in fp32; 1: every P_s rounded to
 // bf16, summed in shard order with a bf16 rounding after each addition, bias added

@@ -14,6 +14,8 @@
 #include "tps_mlp.cuh"
 #include "tps_mlp_sk.cuh"
 #include "tps_attn.cuh"
+#include "tps_cache.cuh"
+#include "tps_sample.cuh"
 #include "tps_internal.h"
 
 namespace tps {
@@ -451,20 +453,51 @@ int launch_argmax_reduce(const void* part, int M, int tp, int per_shard_entries,
 
 int attention_smem_bytes(int two_tiles) { return two_tiles ? kAttn2SmemBytes : kAttnSmemBytes; }
 
-int launch_attention(const CUtensorMap& tqkv, const AttnArgs& a, int two_tiles, int grid, cudaStream_t st) {
-  static unsigned long long attr_done[2] = {0ull, 0ull};
+template <class Kernel>
+static int launch_attn_kernel(Kernel* fn, unsigned long long* attr_done, int threads, int smem,
+                              const CUtensorMap& tqkv, const AttnArgs& a, int grid, cudaStream_t st) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return -6;
   const unsigned long long bit = 1ull << (dev & 63);
-  const int v = two_tiles ? 1 : 0;
-  const int smem = attention_smem_bytes(v);
-  auto* fn = v ? tps_attn2_kernel : tps_attn_kernel;
-  if (!(__atomic_load_n(&attr_done[v], __ATOMIC_ACQUIRE) & bit)) {
+  if (!(__atomic_load_n(attr_done, __ATOMIC_ACQUIRE) & bit)) {
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -6;
-    __atomic_fetch_or(&attr_done[v], bit, __ATOMIC_ACQ_REL);
+    __atomic_fetch_or(attr_done, bit, __ATOMIC_ACQ_REL);
   }
-  LaunchCfg lc(grid, smem, st, 1, v ? kAttn2Threads : kAttnThreads, true);
+  LaunchCfg lc(grid, smem, st, 1, threads, true);
   if (cudaLaunchKernelEx(&lc.cfg, fn, tqkv, a) != cudaSuccess) return -6;
+  return cudaGetLastError() == cudaSuccess ? 0 : -6;
+}
+
+int launch_attention(const CUtensorMap& tqkv, const AttnArgs& a, int two_tiles, int grid, cudaStream_t st) {
+  static unsigned long long attr_done[2] = {0ull, 0ull};
+  return two_tiles ? launch_attn_kernel(tps_attn2_kernel<false>, &attr_done[1], kAttn2Threads, kAttn2SmemBytes, tqkv,
+                                        a, grid, st)
+                   : launch_attn_kernel(tps_attn_kernel, &attr_done[0], kAttnThreads, kAttnSmemBytes, tqkv, a, grid,
+                                        st);
+}
+
+int launch_window_attention(const CUtensorMap& tqkv, const AttnArgs& a, int grid, cudaStream_t st) {
+  static unsigned long long attr_done = 0ull;
+  return launch_attn_kernel(tps_attn2_kernel<true>, &attr_done, kAttn2Threads, kAttn2SmemBytes, tqkv, a, grid, st);
+}
+
+int launch_kv_append(const KvAppendArgs& a, cudaStream_t st) {
+  const long long units = static_cast<long long>(a.nseq) * a.S * a.tp * 2 * a.kvs * 16;
+  const long long grid = (units + kAppendThreads - 1) / kAppendThreads;
+  LaunchCfg lc(static_cast<int>(grid), 0, st, 1, kAppendThreads, true);
+  if (cudaLaunchKernelEx(&lc.cfg, tps_kv_append_kernel, a) != cudaSuccess) return -6;
+  return cudaGetLastError() == cudaSuccess ? 0 : -6;
+}
+
+int launch_decode(const DecodeArgs& a, cudaStream_t st) {
+  LaunchCfg lc(a.nseq * a.nkv, 0, st, 1, kDecThreads, true);
+  if (cudaLaunchKernelEx(&lc.cfg, tps_decode_plain_kernel, a) != cudaSuccess) return -6;
+  return cudaGetLastError() == cudaSuccess ? 0 : -6;
+}
+
+int launch_sample(const SampleArgs& a, cudaStream_t st) {
+  LaunchCfg lc(a.m < 4 * 148 ? a.m : 4 * 148, 0, st, 1, kSampleThreads, true);
+  if (cudaLaunchKernelEx(&lc.cfg, tps_sample_plain_kernel, a) != cudaSuccess) return -6;
   return cudaGetLastError() == cudaSuccess ? 0 : -6;
 }
 

@@ -1,0 +1,551 @@
+"""GPU parity of the serving operators against the fp64 oracle: attention with a sliding
+window and sinks, KV cache append, decode against the caches and behind a shared prefix,
+sampling.
+
+Attention tolerance, element by element. With A = sum_j p_j |v_j| of the element: each
+weight is rounded to bf16 (half a step, 2^-8 of its value), which moves the sum by at
+most 2^-8 A; the exponentials are within 7.5e-5 of their values in the numerator and the
+sum (together below 2^-12 A), the fp32 scores and sums add less than 2^-12 A at these
+sizes; the result is rounded to bf16 once, 2^-8 of itself. So
+|y - ref| <= (2^-8 + 2^-11) A + 2^-8 (1 + 2^-6) |ref| + 2^-126.
+Copies and drawn tokens are exact."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+import workloads as WL
+
+pytestmark = pytest.mark.gpu
+
+D = 128
+
+
+@pytest.fixture(scope="module")
+def T():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import tensor_sharded_linear_columnparallel_b200 as T
+    return T
+
+
+@pytest.fixture(autouse=True)
+def _clean(T):
+    yield
+    torch.cuda.synchronize()
+    assert T.tps_device_error() == T.TPS_OK
+
+
+def f64(t):
+    return t.detach().to("cpu", torch.float64).numpy()
+
+
+def close(y, ref, mag, what=""):
+    y = f64(y)
+    assert y.shape == ref.shape, (what, y.shape, ref.shape)
+    tol = (2.0 ** -8 + 2.0 ** -11) * mag + 2.0 ** -8 * (1 + 2.0 ** -6) * np.abs(ref) + 2.0 ** -126
+    err = np.abs(y - ref)
+    assert np.isfinite(y).all(), what
+    assert (err <= tol).all(), f"{what}: {(err / tol).max():.3f} of the tolerance at {np.unravel_index((err / tol).argmax(), err.shape)}"
+
+
+def geom(hq, hkv, tp):
+    kvs = hkv // tp if hkv % tp == 0 else 1
+    return tp * kvs, tp * (hq // tp + 2 * kvs) * D
+
+
+# ============================================================ window attention
+WINDOWS = [  # nseq, S, hq, hkv, tp, window, nsink, std
+    (1, 1, 2, 1, 1, 1, 0, 1.0),
+    (1, 128, 2, 1, 1, 1, 0, 1.0),        # every query sees itself alone
+    (1, 300, 4, 2, 2, 17, 0, 1.0),
+    (1, 700, 2, 1, 1, 128, 4, 1.0),      # window = block
+    (1, 700, 2, 1, 1, 129, 4, 1.0),
+    (1, 700, 2, 1, 1, 127, 4, 3.0),
+    (2, 641, 4, 4, 4, 200, 130, 1.0),    # sinks over a block border, odd number of query blocks
+    (3, 520, 4, 1, 2, 64, 1, 1.0),       # KV head replicated
+    (1, 900, 7, 1, 1, 256, 128, 1.0),
+    (2, 384, 2, 2, 1, 10 ** 9, 10 ** 9, 1.0),   # plain causal
+    (1, 1500, 2, 1, 1, 300, 4, 1.0),
+    (1, 1025, 2, 1, 1, 2, 1000, 1.0),    # nearly everything is a sink
+    (1, 2048, 2, 2, 2, 512, 0, 6.0),     # peaked softmax
+]
+
+
+@pytest.mark.parametrize("nseq,S,hq,hkv,tp,window,nsink,std", WINDOWS)
+def test_window_attention(T, nseq, S, hq, hkv, tp, window, nsink, std):
+    qkv = WL.gen_normal((nseq * S, geom(hq, hkv, tp)[1]), std, 901)
+    A = T.sharded_window_attention(qkv.cuda(), nseq, S, T.Heads(hq, hkv, D), tp, window, nsink)
+    close(A, *O.window_attention_sharded(qkv, hq, hkv, D, tp, nseq, S, window, nsink))
+    assert torch.equal(A, T.sharded_window_attention(qkv.cuda(), nseq, S, T.Heads(hq, hkv, D), tp, window, nsink))
+
+
+def test_window_attention_many_items_per_cta(T):
+    """More work items than SMs, with and without a second query tile."""
+    nseq, S, hq, hkv, tp, W, ns = 13, 333, 32, 8, 8, 100, 5
+    qkv = WL.gen_normal((nseq * S, geom(hq, hkv, tp)[1]), 1.0, 902)
+    A = T.sharded_window_attention(qkv.cuda(), nseq, S, T.Heads(hq, hkv, D), tp, W, ns)
+    close(A, *O.window_attention_sharded(qkv, hq, hkv, D, tp, nseq, S, W, ns))
+
+
+def test_window_attention_wide_window_equals_causal_attention(T):
+    qkv = WL.gen_normal((2 * 450, geom(8, 2, 2)[1]), 1.0, 903).cuda()
+    A = T.sharded_window_attention(qkv, 2, 450, T.Heads(8, 2, D), 2, 450)
+    assert torch.equal(A, T.sharded_gqa_attention(qkv, 2, 450, T.Heads(8, 2, D), 2, True))
+
+
+def test_window_attention_sequences_do_not_touch(T):
+    """NaN tokens of the next sequence, in the same 128-key block, change nothing; rows
+    behind the last sequence keep their bits."""
+    S = 70
+    qkv = WL.gen_normal((2 * S, geom(2, 1, 1)[1]), 1.0, 904)
+    ref = O.window_attention_sharded(qkv[:S], 2, 1, D, 1, 1, S, 30, 2)
+    bad = qkv.clone()
+    bad[S:] = float("nan")
+    out = torch.full((2 * S + 3, 2 * D), 7.0, dtype=torch.bfloat16, device="cuda")
+    T.sharded_window_attention(bad.cuda(), 2, S, T.Heads(2, 1, D), 1, 30, 2, out=out[:2 * S])
+    close(out[:S], *ref)
+    assert (out[2 * S:] == 7.0).all()
+
+
+# ============================================================ caches
+def caches(nseq, nkv, cap, seed, fill=None):
+    if fill is not None:
+        return [torch.full((nseq, nkv, cap, D), fill, dtype=torch.bfloat16) for _ in range(2)]
+    return [WL.gen_normal((nseq, nkv, cap, D), 1.0, seed + i) for i in range(2)]
+
+
+APPENDS = [  # nseq, S, hq, hkv, tp, cap, nsink, pos, count
+    (1, 1, 2, 1, 1, 1, 0, [5], [1]),
+    (3, 7, 4, 2, 2, 16, 0, [0, 3, 9], [7, 0, 7]),
+    (3, 50, 4, 1, 2, 13, 4, [0, 2, 100], [50, 9, 77]),    # the ring wraps within the call; count above S
+    (4, 5, 8, 8, 4, 9, 8, [-1, 0, 7, 8], [5, 5, 5, -3]),   # unused row, one ring slot
+    (2, 300, 4, 4, 1, 130, 2, None, None),
+    (2, 3, 2, 1, 1, 70, 1, [2 ** 31 - 4, 2 ** 30], [3, 2]),
+]
+
+
+@pytest.mark.parametrize("nseq,S,hq,hkv,tp,cap,nsink,pos,count", APPENDS)
+def test_kv_append_bit_exact(T, nseq, S, hq, hkv, tp, cap, nsink, pos, count):
+    nkv, cols = geom(hq, hkv, tp)
+    qkv = WL.gen_normal((nseq * S, cols), 1.0, 911)
+    k, v = caches(nseq, nkv, cap, 912)
+    kg, vg = k.cuda(), v.cuda()
+    vec = lambda x: None if x is None else torch.tensor(x, dtype=torch.int32, device="cuda")
+    T.sharded_kv_append(qkv.cuda(), nseq, S, T.Heads(hq, hkv, D), tp, kg, vg, pos=vec(pos), count=vec(count), nsink=nsink)
+    kr, vr = f64(k).copy(), f64(v).copy()
+    O.kv_append(qkv, hq, hkv, D, tp, nseq, S, pos or [0] * nseq, count or [S] * nseq, nsink, kr, vr)
+    assert np.array_equal(f64(kg), kr) and np.array_equal(f64(vg), vr)
+
+
+DECODES = [  # hq, hkv, tp, cap, nsink, window, positions
+    (2, 1, 1, 1, 0, 1, [0, 3, -1]),
+    (4, 2, 2, 64, 0, 64, [0, 1, 62, 63, 64, 1000]),
+    (4, 1, 2, 300, 4, 200, [0, 3, 4, 5, 127, 128, 203, 204, 299, 300, 301, 555, -7]),   # KV head replicated
+    (32, 8, 8, 516, 4, 512, [10, 515, 516, 5000]),
+    (7, 1, 1, 260, 130, 130, [129, 130, 131, 259, 260, 700]),                             # sinks over a block border
+    (12, 4, 4, 1000, 1, 37, [0, 36, 37, 38, 998, 999, 1000, 40000]),
+    (16, 1, 1, 200, 0, 190, [199, 200, 389]),
+    (40, 2, 1, 150, 2, 148, [1, 149, 150]),                                               # 20 query heads per KV head
+    (8, 8, 1, 640, 0, 128, [639, 640, 100]),                                              # one query head per KV head
+]
+
+
+@pytest.mark.parametrize("hq,hkv,tp,cap,nsink,window,pos", DECODES)
+@pytest.mark.parametrize("std", [1.0, 4.0])
+def test_window_decode(T, hq, hkv, tp, cap, nsink, window, pos, std):
+    """Against the oracle, with NaN in every slot that no position was written to."""
+    nseq = len(pos)
+    nkv, cols = geom(hq, hkv, tp)
+    h = T.Heads(hq, hkv, D)
+    qkv = WL.gen_normal((nseq, cols), std, 921)
+    k, v = caches(nseq, nkv, cap, 922)
+    for b, t in enumerate(pos):
+        written = {O.cache_slot(j, nsink, cap) for j in range(max(0, t - 2 * cap), t)} | set(range(min(nsink, max(t, 0))))
+        for s in set(range(cap)) - written:
+            k[b, :, s] = float("nan")
+            v[b, :, s] = float("nan")
+    kg, vg, pg = k.cuda(), v.cuda(), torch.tensor(pos, dtype=torch.int32, device="cuda")
+    ws = T.decode_workspace(nseq, h, tp)
+    out = T.sharded_window_decode(qkv.cuda(), h, tp, pg, window, kg, vg, ws, nsink=nsink)
+    kr, vr = f64(k).copy(), f64(v).copy()
+    ref, mag = O.cached_decode(qkv, hq, hkv, D, tp, pos, window, nsink, kr, vr)
+    close(out, ref, mag)
+    assert np.array_equal(f64(kg), kr, equal_nan=True) and np.array_equal(f64(vg), vr, equal_nan=True)
+    again = T.sharded_window_decode(qkv.cuda(), h, tp, pg, window, kg, vg, ws, nsink=nsink)
+    assert torch.equal(out, again)
+    assert T.tps_sync_status(ws) == T.TPS_OK
+
+
+@pytest.mark.parametrize("nseq,cap", [(40, 700), (1, 9000), (3, 4000), (150, 130)])
+def test_window_decode_split_over_ctas(T, nseq, cap):
+    """Work that is cut at any place: ragged positions, one long sequence, more rows than SMs."""
+    hq, hkv, tp = 8, 2, 2
+    nkv, cols = geom(hq, hkv, tp)
+    h = T.Heads(hq, hkv, D)
+    g = torch.Generator().manual_seed(nseq)
+    pos = torch.randint(-1, 2 * cap, (nseq,), generator=g, dtype=torch.int32)
+    if nseq == 1:
+        pos[0] = 3 * cap
+    qkv = WL.gen_normal((nseq, cols), 1.0, 931)
+    k, v = caches(nseq, nkv, cap, 932)
+    kg, vg = k.cuda(), v.cuda()
+    ws = T.decode_workspace(nseq, h, tp)
+    out = T.sharded_window_decode(qkv.cuda(), h, tp, pos.cuda(), cap - 4, kg, vg, ws, nsink=4)
+    kr, vr = f64(k), f64(v)
+    close(out, *O.cached_decode(qkv, hq, hkv, D, tp, pos.tolist(), cap - 4, 4, kr, vr))
+
+
+PREFIXES = [  # hq, hkv, tp, prefix, cap, positions
+    (2, 1, 1, 1, 4, [0]),
+    (4, 2, 2, 0, 40, [0, 39, 40, -1, 7]),
+    (4, 2, 2, 130, 40, [0, 39, 40, -1, 7]),       # pos = cap: unused
+    (32, 8, 8, 1000, 300, [0, 5, 299, 128, 127, 200, -1, 64]),
+    (7, 1, 1, 257, 64, list(range(0, 40, 2))),     # 7 x 20 rows: two query tiles
+    (8, 1, 1, 640, 16, [i % 17 - 1 for i in range(70)]),
+    (4, 1, 2, 5000, 20, [3, 19]),                  # KV head replicated, a prefix split over many CTAs
+    (16, 16, 4, 384, 10, [1, 2, 3]),
+    (40, 2, 1, 200, 8, [0, 7, 3]),                 # 20 query heads per KV head
+]
+
+
+@pytest.mark.parametrize("hq,hkv,tp,prefix,cap,pos", PREFIXES)
+@pytest.mark.parametrize("std", [1.0, 4.0])
+def test_prefix_decode(T, hq, hkv, tp, prefix, cap, pos, std):
+    nseq = len(pos)
+    nkv, cols = geom(hq, hkv, tp)
+    h = T.Heads(hq, hkv, D)
+    qkv = WL.gen_normal((nseq, cols), std, 941)
+    k, v = caches(nseq, nkv, cap, 942)
+    for b, t in enumerate(pos):
+        k[b, :, max(0, t):] = float("nan")
+        v[b, :, max(0, t):] = float("nan")
+    pk, pv = WL.gen_normal((nkv, prefix, D), 1.0, 944), WL.gen_normal((nkv, prefix, D), 1.0, 945)
+    kg, vg, pg = k.cuda(), v.cuda(), torch.tensor(pos, dtype=torch.int32, device="cuda")
+    ws = T.decode_workspace(nseq, h, tp, prefix)
+    args = (pk.cuda(), pv.cuda()) if prefix else (None, None)
+    out = T.sharded_prefix_decode(qkv.cuda(), h, tp, *args, pg, kg, vg, ws)
+    kr, vr = f64(k).copy(), f64(v).copy()
+    live = [t if 0 <= t < cap else -1 for t in pos]
+    ref, mag = O.cached_decode(qkv, hq, hkv, D, tp, live, cap, 0, kr, vr, f64(pk), f64(pv))
+    close(out, ref, mag)
+    assert np.array_equal(f64(kg), kr, equal_nan=True) and np.array_equal(f64(vg), vr, equal_nan=True)
+    assert torch.equal(out, T.sharded_prefix_decode(qkv.cuda(), h, tp, *args, pg, kg, vg, ws))
+    assert T.tps_sync_status(ws) == T.TPS_OK
+
+
+def test_decode_large_scores_and_far_apart_maxima(T):
+    """Scores whose maximum moves by hundreds from block to block, up and down."""
+    hq, hkv, tp, cap, P = 4, 1, 1, 512, 700
+    h = T.Heads(hq, hkv, D)
+    qkv = WL.gen_normal((2, 6 * D), 1.0, 951)
+    k, v = caches(2, 1, cap, 952)
+    pk, pv = WL.gen_normal((1, P, D), 1.0, 953), WL.gen_normal((1, P, D), 1.0, 954)
+    ramp = torch.linspace(0.0, 12.0, cap)[:, None]
+    k[0] = (k[0].float() * ramp).to(torch.bfloat16)
+    k[1] = (k[1].float() * ramp.flip(0)).to(torch.bfloat16)
+    pk[0, 300:310] *= 16
+    pos = [510, 400]
+    for prefix in (False, True):
+        kg, vg = k.cuda(), v.cuda()
+        pg = torch.tensor(pos, dtype=torch.int32, device="cuda")
+        ws = T.decode_workspace(2, h, tp, P if prefix else 0)
+        args = (pk.cuda(), pv.cuda()) if prefix else (None, None)
+        out = T.sharded_prefix_decode(qkv.cuda(), h, tp, *args, pg, kg, vg, ws)
+        ref, mag = O.cached_decode(qkv, hq, hkv, D, tp, pos, cap, 0, f64(k).copy(), f64(v).copy(),
+                                   *((f64(pk), f64(pv)) if prefix else (None, None)))
+        # scores of this size carry an fp32 error of their own: |s| <= 1200, so a weight moves by up
+        # to 1200 * 128 * 2^-24 = 2^-6.7 of itself in the worst order of the 128 products
+        close(out, ref, mag * (1 + 2.0 ** -6.7 / 2.0 ** -8))
+
+
+def test_decode_graph_replay_with_new_positions_on_another_stream(T):
+    """A captured step replays with the positions and tokens of its replay; the workspace
+    serves every replay."""
+    hq, hkv, tp, cap, ns, W, P = 8, 2, 2, 100, 4, 90, 300
+    nkv, cols = geom(hq, hkv, tp)
+    h = T.Heads(hq, hkv, D)
+    n = 3
+    k, v = caches(n, nkv, cap, 961)
+    pk, pv = WL.gen_normal((nkv, P, D), 1.0, 963), WL.gen_normal((nkv, P, D), 1.0, 964)
+    kg, vg, k2, v2, pkg, pvg = k.cuda(), v.cuda(), k.cuda(), v.cuda(), pk.cuda(), pv.cuda()
+    qkv = torch.zeros(n, cols, dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros(n, dtype=torch.int32, device="cuda")
+    ws1, ws2 = T.decode_workspace(n, h, tp), T.decode_workspace(n, h, tp, P)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        for _ in range(2):
+            T.sharded_window_decode(qkv, h, tp, pos, W, kg, vg, ws1, nsink=ns)
+            T.sharded_prefix_decode(qkv, h, tp, pkg, pvg, pos, k2, v2, ws2)
+        st.synchronize()
+        kg.copy_(k), vg.copy_(v), k2.copy_(k), v2.copy_(v)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            a = T.sharded_window_decode(qkv, h, tp, pos, W, kg, vg, ws1, nsink=ns)
+            b = T.sharded_prefix_decode(qkv, h, tp, pkg, pvg, pos, k2, v2, ws2)
+    torch.cuda.synchronize()
+    refs = [f64(x).copy() for x in (k, v, k, v)]
+    for i, p in enumerate([[0, 40, 99], [98, -1, 41], [250, 97, 0]]):
+        x = WL.gen_normal((n, cols), 1.0, 970 + i)
+        qkv.copy_(x), pos.copy_(torch.tensor(p, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        close(a, *O.cached_decode(x, hq, hkv, D, tp, p, W, ns, *refs[:2]))
+        live = [t if t < cap else -1 for t in p]
+        close(b, *O.cached_decode(x, hq, hkv, D, tp, live, cap, 0, *refs[2:], f64(pk), f64(pv)))
+
+
+# ============================================================ sampling
+def sample_ref(logits, u, temperature=None, top_k=None, top_p=None, min_p=None):
+    l = f64(logits)
+    get = lambda x, i, d: d if x is None else float(x[i])
+    r = [O.sample_row(l[i], float(u[i]), get(temperature, i, 1.0), int(get(top_k, i, 0)), get(top_p, i, 1.0),
+                      get(min_p, i, 0.0)) for i in range(l.shape[0])]
+    return np.array([x[0] for x in r]), np.array([x[1] for x in r])
+
+
+def check_sample(T, logits, u, **kw):
+    dev = lambda x: None if x is None else x.cuda()
+    idx, logp = T.logits_sample(logits.cuda(), u.cuda(), **{n: dev(x) for n, x in kw.items()})
+    ri, rl = sample_ref(logits, u, **kw)
+    assert np.array_equal(idx.cpu().numpy(), ri), [(a, b) for a, b in zip(idx.tolist(), ri.tolist()) if a != b][:5]
+    fin = np.isfinite(rl)
+    got = f64(logp)
+    # a share of 2^-44 units: the weight is off by half a unit; the logarithm is rounded to fp32
+    assert np.allclose(got[fin], rl[fin], rtol=2.0 ** -23, atol=1e-6), np.abs(got[fin] - rl[fin]).max()
+    assert np.array_equal(got[~fin], rl[~fin])
+
+
+def rows(m, V, spread, seed, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(m, V, generator=g) * spread).to(dtype), torch.rand(m, generator=g), g
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [8, 96, 1000, 4104, 33008])
+@pytest.mark.parametrize("filters", ["none", "k", "p", "q", "kp", "kpq", "mixed"])
+def test_logits_sample(T, V, dtype, filters):
+    m = 9
+    logits, u, g = rows(m, V, 2.0, V + len(filters), dtype)
+    kw = dict(temperature=0.4 + 1.6 * torch.rand(m, generator=g))
+    if "k" in filters or filters == "mixed":
+        kw["top_k"] = torch.randint(1, min(V, 200) + 1, (m,), generator=g, dtype=torch.int32)
+    if "p" in filters or filters == "mixed":
+        kw["top_p"] = 0.2 + 0.79 * torch.rand(m, generator=g)
+    if "q" in filters or filters == "mixed":
+        kw["min_p"] = 0.2 * torch.rand(m, generator=g)
+    if filters == "mixed":
+        for n, off in (("top_k", 0), ("top_p", 1.0), ("min_p", 0.0)):
+            kw[n][torch.rand(m, generator=g) < 0.4] = off
+        kw["temperature"][:2] = torch.tensor([0.0, -1.0])
+        kw["top_k"][3] = V + 5
+    check_sample(T, logits, u, **kw)
+
+
+def test_logits_sample_defaults_and_extremes(T):
+    logits, _, g = rows(8, 504, 3.0, 5)
+    u = torch.tensor([0.0, 1.0, 0.99999994, -3.0, 7.0, float("nan"), 0.5, 1e-30])
+    ref_u = torch.tensor([0.0, 1.0, 0.99999994, 0.0, 1.0, 0.0, 0.5, 1e-30])
+    idx, _ = T.logits_sample(logits.cuda(), u.cuda())
+    assert np.array_equal(idx.cpu().numpy(), sample_ref(logits, ref_u)[0])
+    hot = torch.tensor([1e-6, 1e-30, 1e30, 0.01, 100.0, float("inf"), float("nan"), 1.0])
+    check_sample(T, logits, torch.rand(8, generator=g), temperature=hot)
+
+
+def test_logits_sample_ties(T):
+    """Equal logits everywhere, and groups of them across the cut of every filter."""
+    m, V = 12, 2048
+    g = torch.Generator().manual_seed(6)
+    u = torch.rand(m, generator=g)
+    flat = torch.zeros(m, V)
+    steps = torch.randint(0, 5, (m, V), generator=g).float()
+    signed = torch.where(torch.rand(m, V, generator=g) < 0.5, torch.tensor(0.0), torch.tensor(-0.0))
+    for l in (flat, steps, signed):
+        check_sample(T, l, u)
+        check_sample(T, l, u, top_k=torch.arange(1, m + 1, dtype=torch.int32) * 37)
+        check_sample(T, l, u, top_p=torch.linspace(0.0, 0.98, m))
+        check_sample(T, l, u, top_k=torch.full((m,), 700, dtype=torch.int32), top_p=torch.linspace(0.03, 0.97, m),
+                     min_p=torch.linspace(0.0, 1.0, m))
+
+
+def test_logits_sample_masked_logits(T):
+    m, V = 10, 1024
+    logits, u, g = rows(m, V, 2.0, 7)
+    logits[torch.rand(m, V, generator=g) < 0.9] = -math.inf
+    logits[1] = -math.inf
+    logits[2] = float("nan")
+    logits[3] = -math.inf
+    logits[3, 1000] = -5.0
+    logits[4, 17] = math.inf
+    logits[5, [3, 900]] = math.inf
+    logits[6] = torch.finfo(torch.float32).min
+    logits[7, ::2] = float("nan")
+    for kw in ({}, dict(top_k=torch.full((m,), 300, dtype=torch.int32)), dict(top_p=torch.full((m,), 0.9)),
+               dict(min_p=torch.full((m,), 0.05)),
+               dict(top_k=torch.full((m,), 5, dtype=torch.int32), top_p=torch.full((m,), 0.7),
+                    temperature=torch.full((m,), 0.5))):
+        check_sample(T, logits, u, **kw)
+
+
+def test_logits_sample_outliers_and_large_vocabulary(T):
+    """One logit far above (or below) the rest, and a vocabulary near the limit: numpy does
+    the sorting here, the definition is the same."""
+    m, V = 4, 262144
+    logits, u, g = rows(m, V, 1.0, 8)
+    logits[1, 77777] = 60.0
+    logits[2, 5] = -3e38
+    logits[3] *= 0.001
+    for k, p in ((0, 1.0), (50, 1.0), (0, 0.9), (100000, 0.95), (3000, 0.5)):
+        idx, _ = T.logits_sample(logits.cuda(), u.cuda(), top_k=torch.full((m,), k, dtype=torch.int32, device="cuda"),
+                                 top_p=torch.full((m,), p, device="cuda"))
+        for i in range(m):
+            l = f64(logits[i])
+            w = np.exp(l - l.max())
+            order = np.lexsort((np.arange(V), -l))[:k or V]
+            pp = float(np.float32(p))
+            if pp < 1:
+                c = np.cumsum(w[order])
+                order = order[np.concatenate([[0.0], c[:-1]]) < pp * c[-1]]
+            kept = np.sort(order)
+            c = np.cumsum(w[kept])
+            assert idx[i].item() == kept[np.searchsorted(c, float(u[i]) * c[-1], side="right")], (i, k, p)
+
+
+def test_logits_sample_frequencies(T):
+    """u on a grid draws every token with its share, within one grid step."""
+    V, n = 16, 4096
+    l = torch.linspace(-2, 2, V)
+    u = (torch.arange(n) + 0.5) / n
+    idx, logp = T.logits_sample(l.repeat(n, 1).cuda().contiguous(), u.cuda())
+    share = np.bincount(idx.cpu().numpy(), minlength=V) / n
+    p = torch.softmax(l.double(), 0).numpy()
+    assert np.abs(share - p).max() <= 1.0 / n
+    assert np.allclose(np.exp(f64(logp)), p[idx.cpu().numpy()], rtol=1e-5)
+
+
+def test_logits_sample_many_rows(T):
+    logits, u, g = rows(1500, 256, 2.0, 9)
+    check_sample(T, logits, u, top_k=torch.randint(0, 40, (1500,), generator=g, dtype=torch.int32),
+                 top_p=0.3 + 0.8 * torch.rand(1500, generator=g))
+
+
+@pytest.mark.parametrize("m,H,V,tp", [(1, 64, 512, 2), (33, 256, 4096, 8), (70, 128, 1000, 1)])
+def test_vocab_parallel_sample_integer_logits(T, m, H, V, tp):
+    """Integer products are exact in fp32, so the drawn token is the oracle's."""
+    X, W = WL.gen_int((m, H), -2, 2, 981), WL.gen_int((H, V), -1, 1, 982)
+    g = torch.Generator().manual_seed(3)
+    u, t = torch.rand(m, generator=g), 2.0 + 6 * torch.rand(m, generator=g)
+    p, k = 0.5 + 0.5 * torch.rand(m, generator=g), torch.randint(0, 60, (m,), generator=g, dtype=torch.int32)
+    pw = T.tp_shard_weights(T.KIND_COLUMN, W.cuda(), tp)
+    idx, logp = T.vocab_parallel_sample(X.cuda(), H, V, tp, pw, u.cuda(), temperature=t.cuda(), top_k=k.cuda(),
+                                        top_p=p.cuda())
+    ri, rl = sample_ref(torch.from_numpy(O.to_f64(X) @ O.to_f64(W)), u, t, k, p)
+    assert np.array_equal(idx.cpu().numpy(), ri)
+    assert np.allclose(f64(logp), rl, rtol=2.0 ** -23, atol=1e-6)
+    greedy, _ = T.vocab_parallel_sample(X.cuda(), H, V, tp, pw, u.cuda(), temperature=torch.zeros(m, device="cuda"))
+    assert torch.equal(greedy, T.vocab_parallel_argmax(X.cuda(), H, V, tp, pw)[0])
+
+
+# ============================================================ together
+def test_prefill_then_decode_with_sampled_tokens(T):
+    """A small model's serving loop: windowed prefill, append, then steps of QKV, decode,
+    o_proj, lm_head and sampling, captured into a graph; every step against the oracle on
+    the values that the step read."""
+    hq, hkv, tp, Hd, V, S, W, ns, steps = 8, 2, 2, 256, 512, 150, 64, 4, 5
+    n, cap = 2, ns + W
+    h = T.Heads(hq, hkv, D)
+    nkv, cols = geom(hq, hkv, tp)
+    Wqkv = WL.gen_normal((Hd, (hq + 2 * hkv) * D), Hd ** -0.5, 991).cuda()
+    Wo = WL.gen_normal((hq * D, Hd), (hq * D) ** -0.5, 992).cuda()
+    Wl = WL.gen_normal((Hd, V), 2 * Hd ** -0.5, 993).cuda()
+    emb = WL.gen_normal((V, Hd), 1.0, 994).cuda()
+    pq = T.tp_shard_weights(T.KIND_QKV, Wqkv, tp, heads=h)
+    po = T.tp_shard_weights(T.KIND_ROW, Wo, tp)
+    pl = T.tp_shard_weights(T.KIND_COLUMN, Wl, tp)
+    tok = torch.randint(0, V, (n, S), generator=torch.Generator().manual_seed(1)).cuda()
+    qkv = T.column_parallel_forward(emb[tok.view(-1)], pq, T.KIND_QKV, (hq + 2 * hkv) * D, tp, heads=h)
+    A = T.sharded_window_attention(qkv, n, S, h, tp, W, ns)
+    close(A, *O.window_attention_sharded(qkv.cpu(), hq, hkv, D, tp, n, S, W, ns))
+    k = torch.full((n, nkv, cap, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    v = k.clone()
+    T.sharded_kv_append(qkv, n, S, h, tp, k, v, nsink=ns)
+    ws = T.decode_workspace(n, h, tp)
+    lws = T.workspace(T.FN_SAMPLE, n, V, Hd, tp)
+    pos = torch.full((n,), S, dtype=torch.int32, device="cuda")
+    u = torch.zeros(n, device="cuda")
+    par = dict(temperature=torch.full((n,), 0.8, device="cuda"), top_k=torch.full((n,), 40, dtype=torch.int32, device="cuda"),
+               top_p=torch.full((n,), 0.9, device="cuda"), min_p=torch.full((n,), 0.02, device="cuda"))
+    cur = tok[:, -1].to(torch.int32).clone()
+
+    def step():
+        x = T.column_parallel_forward(emb[cur.long()], pq, T.KIND_QKV, (hq + 2 * hkv) * D, tp, heads=h)
+        a = T.sharded_window_decode(x, h, tp, pos, W, k, v, ws, nsink=ns)
+        y = T.row_parallel_forward(a, po, Hd, tp)
+        idx, _ = T.vocab_parallel_sample(y, Hd, V, tp, pl, u, lws, **par)
+        cur.copy_(idx)
+        pos.add_(1)
+        return x, a, y, idx
+
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    keep = [t.clone() for t in (k, v, pos, cur)]
+    with torch.cuda.stream(st):
+        step()
+        st.synchronize()
+        for t, s in zip((k, v, pos, cur), keep):
+            t.copy_(s)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            x, a, y, idx = step()
+    torch.cuda.synchronize()
+    kr, vr = f64(k).copy(), f64(v).copy()
+    for i in range(steps):
+        u.copy_(torch.rand(n, generator=torch.Generator().manual_seed(i)))
+        g.replay()
+        torch.cuda.synchronize()
+        close(a, *O.cached_decode(x.cpu(), hq, hkv, D, tp, [S + i] * n, W, ns, kr, vr), what=f"step {i}")
+        # the token from the logits that the step left in its workspace
+        logits = lws[256:256 + n * V * 4].view(torch.float32).view(n, V).cpu()
+        ref = O.to_f64(y.cpu()) @ O.to_f64(Wl.cpu())
+        assert np.abs(f64(logits) - ref).max() <= 1e-4 * (1 + np.abs(ref).max())
+        cpu = {a_: b_.cpu() for a_, b_ in par.items()}
+        assert np.array_equal(idx.cpu().numpy(), sample_ref(logits, u.cpu(), **cpu)[0])
+    assert pos.tolist() == [S + steps] * n
+
+
+def test_refused_calls(T):
+    h = T.Heads(4, 2, D)
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device="cuda")
+    cols = geom(4, 2, 2)[1]
+    k, v, pos, ws = z(2, 2, 8, D), z(2, 2, 8, D), z(2, dtype=torch.int32), T.decode_workspace(2, h, 2)
+    with pytest.raises(ValueError):
+        T.sharded_window_attention(z(4, cols), 1, 5, h, 2, 4)
+    with pytest.raises(ValueError):
+        T.sharded_kv_append(z(4, cols), 2, 2, h, 2, k, z(2, 2, 9, D))
+    with pytest.raises(ValueError):
+        T.sharded_kv_append(z(4, cols), 2, 2, h, 2, k, v, pos=z(3, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        T.sharded_window_decode(z(2, cols), h, 2, z(2, dtype=torch.int64), 4, k, v, ws)
+    with pytest.raises(ValueError):
+        T.sharded_window_decode(z(2, cols), h, 2, pos, 4, k[:, :, ::2], v[:, :, ::2], ws)
+    with pytest.raises(ValueError):
+        T.sharded_prefix_decode(z(2, cols), h, 2, z(2, 5, D), z(2, 6, D), pos, k, v, ws)
+    with pytest.raises(T.TpsError) as e:
+        T.sharded_window_decode(z(2, cols), h, 2, pos, 9, k, v, ws)
+    assert e.value.status == T.TPS_ERR_ARG
+    with pytest.raises(T.TpsError) as e:
+        T.sharded_window_decode(z(2, cols), h, 2, pos, 4, k, v, ws[:64])
+    assert e.value.status == T.TPS_ERR_WORKSPACE
+    with pytest.raises(T.TpsError) as e:
+        T.logits_sample(z(2, 12), z(2, dtype=torch.float32))
+    assert e.value.status == T.TPS_ERR_ALIGN
+    with pytest.raises(ValueError):
+        T.logits_sample(z(2, 16), z(3, dtype=torch.float32))
+    with pytest.raises(ValueError):
+        T.logits_sample(z(2, 16, dtype=torch.float16), z(2, dtype=torch.float32))
+    assert T.logits_sample(z(0, 16), z(0, dtype=torch.float32))[0].numel() == 0
+    assert T.sharded_window_attention(z(0, cols), 0, 5, h, 2, 4).numel() == 0
