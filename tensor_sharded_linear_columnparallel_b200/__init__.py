@@ -14,6 +14,7 @@ Weights use the math orientation W[k, n] (Y = X W) unless ``transposed=True``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -402,78 +403,95 @@ def row_parallel_forward_noalloc(X: torch.Tensor, packed_v: torch.Tensor, n: int
 
 
 # ---------------------------------------------------------------- serving: windows, caches, sampling
+# These calls run many times per second on little work, so their checks cost as little as
+# they can: one pass per tensor, and no device or stream switch where none is needed.
 class _On:
-    """The call's device and stream: checks that its tensors share one device, makes that
-    device current for the call, and allocates outputs on the stream that writes them."""
+    """The call's device and stream: makes the tensors' device current for the call and
+    allocates outputs on the stream that writes them. Yields the raw stream."""
 
-    def __init__(self, stream, *tensors):
-        self.dev = tensors[0].device
-        for t in tensors[1:]:
-            if t is not None and t.device != self.dev:
-                raise ValueError(f"tensors on {self.dev} and {t.device}")
-        self.stream = stream
+    __slots__ = ("dev", "stream", "guard", "on")
+
+    def __init__(self, dev: int, stream):
+        self.dev, self.stream, self.guard, self.on = dev, stream, None, None
 
     def __enter__(self):
+        if self.stream is None and torch.cuda.current_device() == self.dev:
+            return torch.cuda.current_stream().cuda_stream
+        if self.stream is not None and self.stream.device.index != self.dev:
+            raise ValueError(f"stream of {self.stream.device}, tensors on cuda:{self.dev}")
         self.guard = torch.cuda.device(self.dev)
         self.guard.__enter__()
         if self.stream is None:
-            self.stream = torch.cuda.current_stream()
-        elif self.stream.device != self.dev:
-            self.guard.__exit__(None, None, None)
-            raise ValueError(f"stream of {self.stream.device}, tensors on {self.dev}")
+            return torch.cuda.current_stream().cuda_stream
         self.on = torch.cuda.stream(self.stream)
         self.on.__enter__()
         return self.stream.cuda_stream
 
     def __exit__(self, *exc):
-        self.on.__exit__(*exc)
-        self.guard.__exit__(*exc)
+        if self.on is not None:
+            self.on.__exit__(*exc)
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
-def _qkv_cols(heads: Heads, tp: int) -> tuple[int, int]:
-    """Columns of a QKV output row and KV head slots tp*kvs (every shard's KV heads)."""
-    _, qc, _, kc = tp_head_map(heads.hq, heads.hkv, tp)
-    return tp * (qc[0] + 2 * kc[0]) * heads.head_dim, tp * kc[0]
-
-
-def _shape(t: torch.Tensor, shape: tuple, what: str) -> None:
-    if tuple(t.shape) != tuple(shape):
+def _arg(t, what: str, dtype, shape, dev: int | None) -> int | None:
+    """Address of a dense CUDA tensor of the given type and shape (None: any) on device
+    dev (None: any), or None for None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, other arguments on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _caches(k_cache, v_cache, nseq: int, nkv: int, d: int) -> int:
-    _dev(k_cache, "k_cache", torch.bfloat16)
-    _dev(v_cache, "v_cache", torch.bfloat16)
-    if k_cache.dim() != 4:
+def _need(t, what: str):
+    if t is None:
+        raise TypeError(f"{what} must be a torch.Tensor")
+    return t
+
+
+@functools.lru_cache(maxsize=256)
+def _geometry(heads: Heads, tp: int):
+    """(columns of a QKV output row, KV head slots tp*kvs, columns of an attention output
+    row, the C struct)."""
+    _, qc, _, kc = tp_head_map(heads.hq, heads.hkv, tp)
+    return tp * (qc[0] + 2 * kc[0]) * heads.head_dim, tp * kc[0], heads.hq * heads.head_dim, heads.c()
+
+
+def _cache_args(k_cache, v_cache, nseq: int, nkv: int, d: int, dev: int):
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be [nseq, tp*kvs, cap, d]")
     cap = k_cache.shape[2]
-    _shape(k_cache, (nseq, nkv, cap, d), "k_cache")
-    _shape(v_cache, (nseq, nkv, cap, d), "v_cache")
-    return cap
-
-
-def _vec(t, n: int, dtype, what: str):
-    if t is not None:
-        _dev(t, what, dtype)
-        _shape(t, (n,), what)
-    return t
+    shape = (nseq, nkv, cap, d)
+    return (_arg(_need(k_cache, "k_cache"), "k_cache", torch.bfloat16, shape, dev),
+            _arg(_need(v_cache, "v_cache"), "v_cache", torch.bfloat16, shape, dev), cap)
 
 
 def sharded_window_attention(qkv: torch.Tensor, nseq: int, seqlen: int, heads: Heads, tp: int, window: int,
                              nsink: int = 0, out=None, stream=None):
     """sharded_gqa_attention (causal) where query t sees the last `window` tokens, itself
     included, and the first `nsink`. Returns attn_out [nseq*seqlen, hq*d] bf16."""
-    _dev(qkv, "qkv", torch.bfloat16)
+    cols, _, ocols, hd = _geometry(heads, tp)
     m = nseq * seqlen
-    _shape(qkv, (m, _qkv_cols(heads, tp)[0]), "qkv")
-    if out is not None:
-        _dev(out, "out", torch.bfloat16)
-        _shape(out, (m, heads.hq * heads.head_dim), "out")
-    with _On(stream, qkv, out) as st:
+    pq = _arg(_need(qkv, "qkv"), "qkv", torch.bfloat16, (m, cols), None)
+    dev = qkv.get_device()
+    po = _arg(out, "out", torch.bfloat16, (m, ocols), dev)
+    with _On(dev, stream) as st:
         if out is None:
-            out = torch.empty(m, heads.hq * heads.head_dim, dtype=torch.bfloat16, device=qkv.device)
-        _check(lib.sharded_window_attention(_ptr(qkv), nseq, seqlen, _heads_ref(heads), tp, window, nsink, _ptr(out),
-                                            st), "sharded_window_attention")
+            out = torch.empty(m, ocols, dtype=torch.bfloat16, device=qkv.device)
+            po = out.data_ptr()
+        _check(lib.sharded_window_attention(pq, nseq, seqlen, ctypes.byref(hd), tp, window, nsink, po, st),
+               "sharded_window_attention")
     return out
 
 
@@ -481,15 +499,15 @@ def sharded_kv_append(qkv: torch.Tensor, nseq: int, seqlen: int, heads: Heads, t
                       v_cache: torch.Tensor, pos=None, count=None, nsink: int = 0, stream=None) -> None:
     """Writes the K and V of a QKV output to the caches [nseq, tp*kvs, cap, d]: token i of
     sequence b, i < count[b], at position pos[b] + i (int32 [nseq]; None: 0 and seqlen)."""
-    _dev(qkv, "qkv", torch.bfloat16)
-    cols, nkv = _qkv_cols(heads, tp)
-    _shape(qkv, (nseq * seqlen, cols), "qkv")
-    cap = _caches(k_cache, v_cache, nseq, nkv, heads.head_dim)
-    _vec(pos, nseq, torch.int32, "pos")
-    _vec(count, nseq, torch.int32, "count")
-    with _On(stream, qkv, k_cache, v_cache, pos, count) as st:
-        _check(lib.sharded_kv_append(_ptr(qkv), nseq, seqlen, _heads_ref(heads), tp, _ptr(pos), _ptr(count), nsink,
-                                     _ptr(k_cache), _ptr(v_cache), cap, st), "sharded_kv_append")
+    cols, nkv, _, hd = _geometry(heads, tp)
+    pq = _arg(_need(qkv, "qkv"), "qkv", torch.bfloat16, (nseq * seqlen, cols), None)
+    dev = qkv.get_device()
+    pk, pv, cap = _cache_args(k_cache, v_cache, nseq, nkv, heads.head_dim, dev)
+    pp = _arg(pos, "pos", torch.int32, (nseq,), dev)
+    pc = _arg(count, "count", torch.int32, (nseq,), dev)
+    with _On(dev, stream) as st:
+        _check(lib.sharded_kv_append(pq, nseq, seqlen, ctypes.byref(hd), tp, pp, pc, nsink, pk, pv, cap, st),
+               "sharded_kv_append")
 
 
 def tps_decode_workspace_bytes(nseq: int, heads: Heads, tp: int, prefix_len: int = 0) -> int:
@@ -501,7 +519,9 @@ def decode_workspace(nseq: int, heads: Heads, tp: int, prefix_len: int = 0, devi
     dev = torch.device(device or "cuda")
     with torch.cuda.device(dev):
         nbytes = tps_decode_workspace_bytes(nseq, heads, tp, prefix_len)
-    return torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    if nbytes == 0:
+        raise TpsError(TPS_ERR_ARG, "tps_decode_workspace_bytes")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
 
 
 def sharded_window_decode(qkv: torch.Tensor, heads: Heads, tp: int, pos: torch.Tensor, window: int,
@@ -510,22 +530,20 @@ def sharded_window_decode(qkv: torch.Tensor, heads: Heads, tp: int, pos: torch.T
     """One new token per row of qkv: appends it at position pos[b] (int32 [nseq]; negative:
     an unused row, output zero) and returns its attention [nseq, hq*d] bf16 over the last
     `window` positions and the first `nsink`."""
-    _dev(qkv, "qkv", torch.bfloat16)
-    nseq = qkv.shape[0]
-    cols, nkv = _qkv_cols(heads, tp)
-    _shape(qkv, (nseq, cols), "qkv")
-    cap = _caches(k_cache, v_cache, nseq, nkv, heads.head_dim)
-    _vec(_dev(pos, "pos", torch.int32), nseq, torch.int32, "pos")
-    _dev(ws, "ws")
-    if out is not None:
-        _dev(out, "out", torch.bfloat16)
-        _shape(out, (nseq, heads.hq * heads.head_dim), "out")
-    with _On(stream, qkv, k_cache, v_cache, pos, ws, out) as st:
+    cols, nkv, ocols, hd = _geometry(heads, tp)
+    nseq = _need(qkv, "qkv").shape[0]
+    pq = _arg(qkv, "qkv", torch.bfloat16, (nseq, cols), None)
+    dev = qkv.get_device()
+    pk, pv, cap = _cache_args(k_cache, v_cache, nseq, nkv, heads.head_dim, dev)
+    pp = _arg(_need(pos, "pos"), "pos", torch.int32, (nseq,), dev)
+    pw = _arg(_need(ws, "ws"), "ws", None, None, dev)
+    po = _arg(out, "out", torch.bfloat16, (nseq, ocols), dev)
+    with _On(dev, stream) as st:
         if out is None:
-            out = torch.empty(nseq, heads.hq * heads.head_dim, dtype=torch.bfloat16, device=qkv.device)
-        _check(lib.sharded_window_decode(_ptr(qkv), nseq, _heads_ref(heads), tp, _ptr(pos), window, nsink,
-                                         _ptr(k_cache), _ptr(v_cache), cap, _ptr(out), _ptr(ws),
-                                         ws.numel() * ws.element_size(), st), "sharded_window_decode")
+            out = torch.empty(nseq, ocols, dtype=torch.bfloat16, device=qkv.device)
+            po = out.data_ptr()
+        _check(lib.sharded_window_decode(pq, nseq, ctypes.byref(hd), tp, pp, window, nsink, pk, pv, cap, po, pw,
+                                         ws.nbytes, st), "sharded_window_decode")
     return out
 
 
@@ -535,41 +553,44 @@ def sharded_prefix_decode(qkv: torch.Tensor, heads: Heads, tp: int, prefix_k, pr
     share (None: no prefix): appends it at position pos[b] of its own linear cache (a row
     with pos[b] outside [0, cap) is unused, output zero) and returns its attention
     [nseq, hq*d] bf16 over the prefix and positions 0..pos[b]."""
-    _dev(qkv, "qkv", torch.bfloat16)
-    nseq = qkv.shape[0]
-    cols, nkv = _qkv_cols(heads, tp)
-    _shape(qkv, (nseq, cols), "qkv")
-    cap = _caches(k_cache, v_cache, nseq, nkv, heads.head_dim)
-    P = 0
+    cols, nkv, ocols, hd = _geometry(heads, tp)
+    nseq = _need(qkv, "qkv").shape[0]
+    pq = _arg(qkv, "qkv", torch.bfloat16, (nseq, cols), None)
+    dev = qkv.get_device()
+    pk, pv, cap = _cache_args(k_cache, v_cache, nseq, nkv, heads.head_dim, dev)
+    P, fk, fv = 0, None, None
     if prefix_k is not None or prefix_v is not None:
-        _dev(prefix_k, "prefix_k", torch.bfloat16)
-        _dev(prefix_v, "prefix_v", torch.bfloat16)
-        P = prefix_k.shape[1] if prefix_k.dim() == 3 else -1
-        _shape(prefix_k, (nkv, P, heads.head_dim), "prefix_k")
-        _shape(prefix_v, (nkv, P, heads.head_dim), "prefix_v")
-    _vec(_dev(pos, "pos", torch.int32), nseq, torch.int32, "pos")
-    _dev(ws, "ws")
-    if out is not None:
-        _dev(out, "out", torch.bfloat16)
-        _shape(out, (nseq, heads.hq * heads.head_dim), "out")
-    with _On(stream, qkv, k_cache, v_cache, pos, ws, out, prefix_k, prefix_v) as st:
+        P = _need(prefix_k, "prefix_k").shape[1] if prefix_k.dim() == 3 else -1
+        fk = _arg(prefix_k, "prefix_k", torch.bfloat16, (nkv, P, heads.head_dim), dev)
+        fv = _arg(_need(prefix_v, "prefix_v"), "prefix_v", torch.bfloat16, (nkv, P, heads.head_dim), dev)
+    pp = _arg(_need(pos, "pos"), "pos", torch.int32, (nseq,), dev)
+    pw = _arg(_need(ws, "ws"), "ws", None, None, dev)
+    po = _arg(out, "out", torch.bfloat16, (nseq, ocols), dev)
+    with _On(dev, stream) as st:
         if out is None:
-            out = torch.empty(nseq, heads.hq * heads.head_dim, dtype=torch.bfloat16, device=qkv.device)
-        _check(lib.sharded_prefix_decode(_ptr(qkv), nseq, _heads_ref(heads), tp, _ptr(prefix_k), _ptr(prefix_v), P,
-                                         _ptr(pos), _ptr(k_cache), _ptr(v_cache), cap, _ptr(out), _ptr(ws),
-                                         ws.numel() * ws.element_size(), st), "sharded_prefix_decode")
+            out = torch.empty(nseq, ocols, dtype=torch.bfloat16, device=qkv.device)
+            po = out.data_ptr()
+        _check(lib.sharded_prefix_decode(pq, nseq, ctypes.byref(hd), tp, fk, fv, P, pp, pk, pv, cap, po, pw,
+                                         ws.nbytes, st), "sharded_prefix_decode")
     return out
 
 
-def _sample_params(m, u, temperature, top_k, top_p, min_p, out_idx, out_logp):
-    _vec(_dev(u, "u", torch.float32), m, torch.float32, "u")
-    _vec(temperature, m, torch.float32, "temperature")
-    _vec(top_k, m, torch.int32, "top_k")
-    _vec(top_p, m, torch.float32, "top_p")
-    _vec(min_p, m, torch.float32, "min_p")
-    _vec(out_idx, m, torch.int32, "out_idx")
-    _vec(out_logp, m, torch.float32, "out_logp")
-    return u, temperature, top_k, top_p, min_p, out_idx, out_logp
+def _sample_args(m, dev, u, temperature, top_k, top_p, min_p, out_idx, out_logp):
+    f32, i32 = torch.float32, torch.int32
+    return [_arg(_need(u, "u"), "u", f32, (m,), dev), _arg(temperature, "temperature", f32, (m,), dev),
+            _arg(top_k, "top_k", i32, (m,), dev), _arg(top_p, "top_p", f32, (m,), dev),
+            _arg(min_p, "min_p", f32, (m,), dev), _arg(out_idx, "out_idx", i32, (m,), dev),
+            _arg(out_logp, "out_logp", f32, (m,), dev)]
+
+
+def _sample_outputs(m, device, par, out_idx, out_logp):
+    if out_idx is None:
+        out_idx = torch.empty(m, dtype=torch.int32, device=device)
+        par[5] = out_idx.data_ptr()
+    if out_logp is None:
+        out_logp = torch.empty(m, dtype=torch.float32, device=device)
+        par[6] = out_logp.data_ptr()
+    return out_idx, out_logp
 
 
 def logits_sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None,
@@ -578,18 +599,15 @@ def logits_sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k
     [m]: temperature, top-k, top-p, min-p (per-row tensors or None), then the inverse of
     the kept weights' running sum in vocabulary order. Returns (indices int32 [m], log of
     the drawn tokens' shares fp32 [m])."""
-    _dev(logits, "logits")
+    pl = _arg(_need(logits, "logits"), "logits", None, None, None)
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D")
     m, V = logits.shape
-    par = _sample_params(m, u, temperature, top_k, top_p, min_p, out_idx, out_logp)
-    with _On(stream, logits, *par) as st:
-        if out_idx is None:
-            out_idx = torch.empty(m, dtype=torch.int32, device=logits.device)
-        if out_logp is None:
-            out_logp = torch.empty(m, dtype=torch.float32, device=logits.device)
-        _check(lib.logits_sample(_ptr(logits), _ydtype(logits.dtype), m, V, _ptr(u), _ptr(temperature), _ptr(top_k),
-                                 _ptr(top_p), _ptr(min_p), _ptr(out_idx), _ptr(out_logp), st), "logits_sample")
+    dev = logits.get_device()
+    par = _sample_args(m, dev, u, temperature, top_k, top_p, min_p, out_idx, out_logp)
+    with _On(dev, stream) as st:
+        out_idx, out_logp = _sample_outputs(m, logits.device, par, out_idx, out_logp)
+        _check(lib.logits_sample(pl, _ydtype(logits.dtype), m, V, *par, st), "logits_sample")
     return out_idx, out_logp
 
 
@@ -598,23 +616,18 @@ def vocab_parallel_sample(X: torch.Tensor, H: int, V: int, tp: int, packed_w: to
                           out_idx=None, out_logp=None, stream=None):
     """logits_sample over a vocab-parallel lm_head (COLUMN pack of W[H, V]); ws is a
     workspace(FN_SAMPLE, m, V, H, tp), which receives the fp32 logits."""
-    _dev(X, "X", torch.bfloat16)
-    _dev(packed_w, "packed_w", torch.bfloat16)
-    m = X.shape[0]
-    _shape(X, (m, H), "X")
-    if packed_w.numel() * 2 < tp_packed_bytes(KIND_COLUMN, H, V, tp):
+    m = _need(X, "X").shape[0]
+    px = _arg(X, "X", torch.bfloat16, (m, H), None)
+    dev = X.get_device()
+    pw = _arg(_need(packed_w, "packed_w"), "packed_w", torch.bfloat16, None, dev)
+    if packed_w.nbytes < tp_packed_bytes(KIND_COLUMN, H, V, tp):
         raise ValueError("packed_w is smaller than the COLUMN pack of W[H, V]")
-    if ws is not None:
-        _dev(ws, "ws")
-    par = _sample_params(m, u, temperature, top_k, top_p, min_p, out_idx, out_logp)
-    with _On(stream, X, packed_w, ws, *par) as st:
+    _arg(ws, "ws", None, None, dev)
+    par = _sample_args(m, dev, u, temperature, top_k, top_p, min_p, out_idx, out_logp)
+    with _On(dev, stream) as st:
         if ws is None:
             ws = workspace(FN_SAMPLE, m, V, H, tp, device=X.device)
-        if out_idx is None:
-            out_idx = torch.empty(m, dtype=torch.int32, device=X.device)
-        if out_logp is None:
-            out_logp = torch.empty(m, dtype=torch.float32, device=X.device)
-        _check(lib.vocab_parallel_sample(_ptr(X), m, H, _ptr(packed_w), V, tp, _ptr(u), _ptr(temperature),
-                                         _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(out_idx), _ptr(out_logp),
-                                         _ptr(ws), ws.numel() * ws.element_size(), st), "vocab_parallel_sample")
+        out_idx, out_logp = _sample_outputs(m, X.device, par, out_idx, out_logp)
+        _check(lib.vocab_parallel_sample(px, m, H, pw, V, tp, *par, ws.data_ptr(), ws.nbytes, st),
+               "vocab_parallel_sample")
     return out_idx, out_logp
