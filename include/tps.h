@@ -393,7 +393,8 @@ TPS_API int sharded_window_decode(const void* qkv, int64_t nseq, const tps_heads
  *   prefix: every new token sees the prefix_len prefix keys and then the positions
  *   0..pos[b] of its own linear cache (nsink = 0). The prefix is read once for the whole
  *   batch. prefix_k, prefix_v: device bf16 [tp*kvs][prefix_len][d] (ignored, may be NULL,
- *   when prefix_len = 0). pos[b] counts the tokens behind the prefix; a row with pos[b]
+ *   when prefix_len = 0; at most 128 query heads per KV head of a shard otherwise,
+ *   TPS_ERR_UNIMPLEMENTED). pos[b] counts the tokens behind the prefix; a row with pos[b]
  *   outside [0, cap) is unused as above. ws: at least
  *   tps_decode_workspace_bytes(nseq, heads, tp, prefix_len) bytes.
  */

@@ -1177,17 +1177,56 @@ int cache_geom(const tps_heads* heads, int tp, int64_t nsink, int64_t cap, HeadM
   return TPS_OK;
 }
 
-size_t decode_ws(int64_t nseq, const HeadMap& hm, int tp, int64_t prefix_len, int sms) {
-  (void)nseq, (void)hm, (void)tp, (void)prefix_len, (void)sms;
-  return kHdr;
+// Workspace of a decode step: header, item counters, the decode kernel's parts, then the
+// prefix kernel's max / sum and parts.
+struct DecodeWs {
+  int nch;                      // chunks of 16 query heads per KV head slot
+  int bpt, tiles, splits, nkb;  // prefix kernel: sequences per tile, tiles, parts of the key blocks
+  size_t counters, parts, ml, prefix_parts, bytes;
+};
+
+DecodeWs decode_ws(int64_t nseq, const HeadMap& hm, int64_t nkv, int64_t prefix_len, int sms) {
+  DecodeWs w{};
+  const int G = hm.qs / hm.kvs;
+  w.nch = (G + 15) / 16;
+  size_t at = kHdr;
+  w.counters = at;
+  at += round256(static_cast<size_t>(nseq) * nkv * w.nch * 4);
+  w.parts = at;
+  at += round256(static_cast<size_t>(sms) * 3 * tps::kDecPartFloats * 4);
+  if (prefix_len > 0 && G <= 128) {
+    w.bpt = 128 / G;
+    w.tiles = static_cast<int>((nseq + w.bpt - 1) / w.bpt);
+    w.nkb = static_cast<int>((prefix_len + 127) / 128);
+    // Parts of the key blocks: the fewest block times on the critical path, a part costing
+    // about three blocks more than its own (start, output, merge).
+    const int64_t pairs = nkv * ((w.tiles + 1) / 2);
+    int64_t best = -1;
+    for (int n = 1; n <= std::min(w.nkb, sms); ++n) {
+      const int64_t waves = (pairs * n + sms - 1) / sms;
+      const int64_t cost = waves * ((w.nkb + n - 1) / n + 3);
+      if (best < 0 || cost < best) {
+        best = cost;
+        w.splits = n;
+      }
+    }
+    const size_t np = static_cast<size_t>(nkv) * w.tiles * w.splits;
+    w.ml = at;
+    at += np * 256 * 4;
+    w.prefix_parts = at;
+    at += np * 128 * 128 * 4;
+  }
+  w.bytes = at;
+  return w;
 }
 
-// One decode step; *a carries the mask and the prefix.
-int run_decode(const void* qkv, int64_t nseq, const tps_heads* heads, const HeadMap& hm, int tp, const int32_t* pos,
-               void* k_cache, void* v_cache, int64_t cap, void* attn_out, void* ws, size_t ws_bytes,
-               tps::DecodeArgs* a, cudaStream_t st) {
+// One decode step; *a carries the mask.
+int run_decode(const void* qkv, int64_t nseq, const tps_heads* heads, const HeadMap& hm, int tp, const void* prefix_k,
+               const void* prefix_v, int64_t prefix_len, const int32_t* pos, void* k_cache, void* v_cache,
+               int64_t cap, void* attn_out, void* ws, size_t ws_bytes, tps::DecodeArgs* a, cudaStream_t st) {
   const int64_t nkv = static_cast<int64_t>(tp) * hm.kvs;
-  if (nseq < 0 || nseq > (1LL << 24) || nseq * nkv > (1LL << 30)) return TPS_ERR_ARG;
+  if (nseq < 0 || nseq > (1LL << 24) || nseq * nkv > (1LL << 26)) return TPS_ERR_ARG;
+  if (prefix_len > 0 && hm.qs / hm.kvs > 128) return TPS_ERR_UNIMPLEMENTED;   // a prefix tile has 128 query rows
   if (nseq == 0) return TPS_OK;
   if (qkv == nullptr || pos == nullptr || k_cache == nullptr || v_cache == nullptr || attn_out == nullptr ||
       ws == nullptr)
@@ -1196,25 +1235,74 @@ int run_decode(const void* qkv, int64_t nseq, const tps_heads* heads, const Head
       !aligned16(ws))
     return TPS_ERR_ALIGN;
   const int sms = num_sms_current();
-  if (ws_bytes < decode_ws(nseq, hm, tp, a->prefix_len, sms)) return TPS_ERR_WORKSPACE;
-  const int rc = check_device();
+  const DecodeWs lay = decode_ws(nseq, hm, nkv, prefix_len, sms);
+  if (ws_bytes < lay.bytes) return TPS_ERR_WORKSPACE;
+  int rc = check_device();
   if (rc) return rc;
+  const int d = heads->head_dim;
+  char* wsp = static_cast<char*>(ws);
   a->qkv = static_cast<const __nv_bfloat16*>(qkv);
   a->nseq = static_cast<int>(nseq);
   a->tp = tp;
   a->qs = hm.qs;
   a->kvs = hm.kvs;
   a->nkv = static_cast<int>(nkv);
-  a->shard_cols = (hm.qs + 2 * hm.kvs) * heads->head_dim;
+  a->shard_cols = (hm.qs + 2 * hm.kvs) * d;
   a->ld = static_cast<long long>(tp) * a->shard_cols;
   a->pos = pos;
   a->cap = static_cast<int>(cap);
   a->k = static_cast<__nv_bfloat16*>(k_cache);
   a->v = static_cast<__nv_bfloat16*>(v_cache);
-  a->scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(heads->head_dim)));
+  a->scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
   a->out = static_cast<__nv_bfloat16*>(attn_out);
-  a->ldo = heads->hq * heads->head_dim;
-  return tps::launch_decode(*a, st) == 0 ? TPS_OK : TPS_ERR_CUDA;
+  a->ldo = heads->hq * d;
+  a->nch = lay.nch;
+  a->counters = reinterpret_cast<int*>(wsp + lay.counters);
+  a->parts = reinterpret_cast<float*>(wsp + lay.parts);
+  a->timeout_ns = kTimeoutNs;
+  a->status = ws_status(ws, ws_bytes);
+  const uint64_t row = static_cast<uint64_t>(d) * 2;
+  const uint64_t ucap = static_cast<uint64_t>(cap), planes = static_cast<uint64_t>(nseq * nkv);
+  CUtensorMap tk, tv;
+  rc = make_map(&tk, k_cache, d, ucap, planes, row, row * ucap, 128, 1);
+  if (rc == TPS_OK) rc = make_map(&tv, v_cache, d, ucap, planes, row, row * ucap, 128, 1);
+  if (rc) return rc;
+  if (prefix_len > 0) {
+    tps::AttnArgs p{};
+    p.nseq = a->nseq;
+    p.S = static_cast<int>(prefix_len);
+    p.qs = hm.qs;
+    p.grp = hm.qs / hm.kvs;
+    p.kvs = hm.kvs;
+    p.nkb = lay.nkb;
+    p.scale_log2 = a->scale_log2;
+    p.timeout_ns = kTimeoutNs;
+    p.status = a->status;
+    p.parts = reinterpret_cast<float*>(wsp + lay.prefix_parts);
+    p.ml = reinterpret_cast<float*>(wsp + lay.ml);
+    p.nkv = a->nkv;
+    p.bpt = lay.bpt;
+    p.tiles = lay.tiles;
+    p.splits = lay.splits;
+    const int64_t items = nkv * ((lay.tiles + 1) / 2) * lay.splits;
+    if (items > (1LL << 30)) return TPS_ERR_ARG;
+    p.items = static_cast<int>(items);
+    CUtensorMap tq, tpk, tpv;
+    // a QKV row as heads of 128 columns: one box is the query heads of one KV head slot of bpt rows
+    const uint64_t hrow = static_cast<uint64_t>(a->ld) / d, P = static_cast<uint64_t>(prefix_len);
+    rc = make_map(&tq, qkv, d, hrow, static_cast<uint64_t>(nseq), row, row * hrow, p.grp, lay.bpt);
+    if (rc == TPS_OK) rc = make_map(&tpk, prefix_k, d, P, static_cast<uint64_t>(nkv), row, row * P, 128, 1);
+    if (rc == TPS_OK) rc = make_map(&tpv, prefix_v, d, P, static_cast<uint64_t>(nkv), row, row * P, 128, 1);
+    if (rc) return rc;
+    if (tps::launch_prefix_attention(tq, tpk, tpv, p, p.items < sms ? p.items : sms, st) != 0) return TPS_ERR_CUDA;
+    a->prefix_parts = p.parts;
+    a->prefix_ml = p.ml;
+    a->prefix_tiles = lay.tiles;
+    a->prefix_splits = lay.splits;
+  }
+  const int64_t blocks = nseq * nkv * lay.nch * ((cap + 127) / 128);   // at most
+  return tps::launch_decode(tk, tv, *a, static_cast<int>(std::min<int64_t>(blocks, sms)), st) == 0 ? TPS_OK
+                                                                                                  : TPS_ERR_CUDA;
 }
 
 }  // namespace
@@ -1614,7 +1702,7 @@ size_t tps_decode_workspace_bytes(int64_t nseq, const tps_heads* heads, int tp, 
   if (nseq < 0 || nseq > (1LL << 24) || prefix_len < 0 || prefix_len > (1LL << 30) ||
       cache_geom(heads, tp, 0, 1, &hm) != TPS_OK)
     return 0;
-  return decode_ws(nseq, hm, tp, prefix_len, num_sms_current());
+  return decode_ws(nseq, hm, static_cast<int64_t>(tp) * hm.kvs, prefix_len, num_sms_current()).bytes;
 }
 
 int sharded_window_decode(const void* qkv, int64_t nseq, const tps_heads* heads, int tp, const int32_t* pos,
@@ -1628,8 +1716,8 @@ int sharded_window_decode(const void* qkv, int64_t nseq, const tps_heads* heads,
   tps::DecodeArgs a{};
   a.window = static_cast<int>(window);
   a.nsink = static_cast<int>(nsink);
-  return run_decode(qkv, nseq, heads, hm, tp, pos, k_cache, v_cache, cap, attn_out, ws, ws_bytes, &a,
-                    static_cast<cudaStream_t>(stream));
+  return run_decode(qkv, nseq, heads, hm, tp, nullptr, nullptr, 0, pos, k_cache, v_cache, cap, attn_out, ws, ws_bytes,
+                    &a, static_cast<cudaStream_t>(stream));
 }
 
 int sharded_prefix_decode(const void* qkv, int64_t nseq, const tps_heads* heads, int tp, const void* prefix_k,
@@ -1644,11 +1732,8 @@ int sharded_prefix_decode(const void* qkv, int64_t nseq, const tps_heads* heads,
   tps::DecodeArgs a{};
   a.window = static_cast<int>(cap);
   a.linear = 1;
-  a.pk = static_cast<const __nv_bfloat16*>(prefix_k);
-  a.pv = static_cast<const __nv_bfloat16*>(prefix_v);
-  a.prefix_len = static_cast<int>(prefix_len);
-  return run_decode(qkv, nseq, heads, hm, tp, pos, k_cache, v_cache, cap, attn_out, ws, ws_bytes, &a,
-                    static_cast<cudaStream_t>(stream));
+  return run_decode(qkv, nseq, heads, hm, tp, prefix_k, prefix_v, prefix_len, pos, k_cache, v_cache, cap, attn_out, ws,
+                    ws_bytes, &a, static_cast<cudaStream_t>(stream));
 }
 
 int logits_sample(const void* logits, int logits_dtype, int64_t m, int64_t V, const float* u,

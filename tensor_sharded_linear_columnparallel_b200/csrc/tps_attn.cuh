@@ -530,6 +530,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // the pipeline above needs. When the sinks reach the windows the item streams 0..last.
 // The tensor map then has the sequence as its third dimension, so the keys behind a
 // sequence's end read as zeros instead of the next sequence's tokens.
+//
+// PREFIX: the queries are one new token of every sequence of a batch, the keys a prefix
+// that they share. A tile is the rows of one KV head slot's query heads of up to 128 / grp
+// sequences, gathered by one box of the QKV row's tensor map; K and V have maps of their
+// own; the items are (slot, pair of tiles, part of the key blocks). The output is left
+// unnormalised with its max and sum for the decode kernel to merge.
+enum : int { ATTN_FULL = 0, ATTN_WINDOW = 1, ATTN_PREFIX = 2 };
 constexpr int kAttn2Stages = 2;                                        // K and V ring stages
 constexpr int kAttnPolyEvery = 4;                                      // exp2 pairs per FMA-polynomial pair
 constexpr int kAttn2Threads = (2 + kAttnSoftWarps) * 32;               // loads, MMA, 2 x 4 softmax warps
@@ -551,6 +558,7 @@ struct AttnPair {
   int qcol, kcol, vcol;
   int fB;                  // WINDOW: first streamed block of tile B (0 or 1)
   int w0, ins;             // WINDOW: first window block; sink blocks streamed after it
+  int split;               // PREFIX: part of the key blocks, which begin at w0; seq is the KV head slot
 };
 
 // WINDOW: key block of streamed block j.
@@ -560,9 +568,24 @@ __device__ __forceinline__ int attn_window_block(const AttnPair& t, int j) {
 
 // Items are numbered heaviest first: band 0 holds the last pair of query blocks of
 // every (sequence, head).
-template <bool WINDOW>
+template <int FORM>
 __device__ __forceinline__ AttnPair attn_pair(const AttnArgs& a, int item) {
   AttnPair t;
+  if constexpr (FORM == ATTN_PREFIX) {
+    const int npairs = (a.tiles + 1) >> 1;
+    t.split = item % a.splits;
+    const int k = item / a.splits;
+    t.seq = k / npairs;
+    t.qa = 2 * (k - t.seq * npairs);
+    t.w0 = static_cast<int>(static_cast<long long>(a.nkb) * t.split / a.splits);
+    t.nblk = static_cast<int>(static_cast<long long>(a.nkb) * (t.split + 1) / a.splits) - t.w0;
+    t.nA = t.nblk;
+    t.nB = t.qa + 1 < a.tiles ? t.nblk : 0;
+    const int r = t.seq / a.kvs;
+    t.h = r * (a.qs + 2 * a.kvs) + (t.seq - r * a.kvs) * a.grp;   // first query head, counted along a QKV row
+    t.qcol = t.kcol = t.vcol = t.fB = t.ins = 0;
+    return t;
+  }
   const int npairs = (a.nqb + 1) >> 1;
   const int per = a.nseq * a.hq;
   const int band = item / per;
@@ -575,7 +598,7 @@ __device__ __forceinline__ AttnPair attn_pair(const AttnArgs& a, int item) {
   t.nB = has_b ? (a.causal ? t.qa + 2 : a.nkb) : 0;
   t.nblk = t.nA > t.nB ? t.nA : t.nB;
   t.fB = t.w0 = t.ins = 0;
-  if constexpr (WINDOW) {
+  if constexpr (FORM == ATTN_WINDOW) {
     const int lo = t.qa * kAttnBlk - a.window + 1;      // first key that tile A's first row sees
     const int nsb = (a.nsink + kAttnBlk - 1) / kAttnBlk;
     if (lo > 0 && lo / kAttnBlk > nsb) {
@@ -634,9 +657,11 @@ __device__ __forceinline__ uint32_t bits_below(int n, int at) {
   return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u);
 }
 
-template <bool WINDOW>
+template <int FORM>
 __global__ void __launch_bounds__(kAttn2Threads, 1)
-    tps_attn2_kernel(const __grid_constant__ CUtensorMap tmQKV, const AttnArgs a) {
+    tps_attn2_kernel(const __grid_constant__ CUtensorMap tmQKV, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
+  constexpr bool WINDOW = FORM == ATTN_WINDOW, PREFIX = FORM == ATTN_PREFIX;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -682,6 +707,10 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
     *never_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmQKV);
+    if constexpr (PREFIX) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -692,6 +721,8 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const uint64_t tmo = a.timeout_ns;
+  // the decode kernel behind the prefix kernel relies on this order (tps_cache.cuh)
+  if constexpr (PREFIX) griddep_wait();
   griddep_launch_dependents();
 
   if (warp == 0) {
@@ -705,13 +736,19 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
       bool ok = true;
       griddep_wait();
       for (int item = attn_item_of(0); ok && item < a.items; ++it, item = attn_item_of(it)) {
-        const AttnPair t = attn_pair<WINDOW>(a, item);
-        const int row0 = WINDOW ? 0 : t.seq * a.S;
-        const int seq = WINDOW ? t.seq : 0;
+        const AttnPair t = attn_pair<FORM>(a, item);
+        const int row0 = FORM == ATTN_FULL ? t.seq * a.S : 0;
+        const int seq = FORM == ATTN_FULL ? 0 : t.seq;
         if (!mbar_wait(q_empty, static_cast<uint32_t>(it & 1) ^ 1u, abort_flag, tmo, a.status)) { ok = false; break; }
         const int ntiles = t.nB > 0 ? 2 : 1;
-        mbar_arrive_expect_tx(q_full, ntiles * kAttnTileBytes);
+        if constexpr (PREFIX) mbar_arrive_expect_tx(q_full, ntiles * a.bpt * a.grp * 256);
+        else mbar_arrive_expect_tx(q_full, ntiles * kAttnTileBytes);
         for (int x = 0; x < ntiles; ++x) {
+          if constexpr (PREFIX) {
+            tma_load_3d(sQ + x * kAttnTileBytes, &tmQKV, q_full, 0, t.h, (t.qa + x) * a.bpt);
+            tma_load_3d(sQ + x * kAttnTileBytes + kAttnHalf, &tmQKV, q_full, 64, t.h, (t.qa + x) * a.bpt);
+            continue;
+          }
           const int r = row0 + (t.qa + x) * kAttnBlk;
           tma_load_3d(sQ + x * kAttnTileBytes, &tmQKV, q_full, t.qcol, r, seq);
           tma_load_3d(sQ + x * kAttnTileBytes + kAttnHalf, &tmQKV, q_full, t.qcol + 64, r, seq);
@@ -728,9 +765,10 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
             const uint32_t dst = (kv ? sV : sK) + st * kAttnTileBytes;
             const int col = kv ? t.vcol : t.kcol;
             mbar_arrive_expect_tx(ful, kAttnTileBytes);
-            const int kb = WINDOW ? attn_window_block(t, j) : j;
-            tma_load_3d(dst, &tmQKV, ful, col, row0 + kb * kAttnBlk, seq);
-            tma_load_3d(dst + kAttnHalf, &tmQKV, ful, col + 64, row0 + kb * kAttnBlk, seq);
+            const int kb = WINDOW ? attn_window_block(t, j) : t.w0 + j;   // w0 = 0 in the full form
+            const CUtensorMap* tm = PREFIX ? (kv ? &tmV : &tmK) : &tmQKV;
+            tma_load_3d(dst, tm, ful, col, row0 + kb * kAttnBlk, seq);
+            tma_load_3d(dst + kAttnHalf, tm, ful, col + 64, row0 + kb * kAttnBlk, seq);
           }
           if (!ok) {   // K of this block may be in flight: count the block
             ++n;
@@ -772,7 +810,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
         umma_commit(s_full(x));
       };
       for (int item = attn_item_of(0); ok && item < a.items; ++it, item = attn_item_of(it)) {
-        const AttnPair t = attn_pair<WINDOW>(a, item);
+        const AttnPair t = attn_pair<FORM>(a, item);
         const int nx[2] = {t.nA, t.nB};               // streamed blocks [fx, nx) of each tile
         const int fx[2] = {0, WINDOW ? t.fB : 0};
         if (!mbar_wait(q_full, static_cast<uint32_t>(it & 1), abort_flag, tmo, a.status)) { ok = false; break; }
@@ -862,7 +900,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
     int it = 0;
     bool ok = true;
     for (int item = attn_item_of(0); ok && item < a.items; ++it, item = attn_item_of(it)) {
-      const AttnPair t = attn_pair<WINDOW>(a, item);
+      const AttnPair t = attn_pair<FORM>(a, item);
       const int nb = x ? t.nB : t.nA;
       if (nb == 0) continue;                      // no tile B in this item
       const int fb = (WINDOW && x) ? t.fB : 0;    // streamed blocks [fb, nb)
@@ -878,12 +916,12 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
           break;
         }
         tc_fence_after();
-        const int kb = WINDOW ? attn_window_block(t, j) : j;
+        const int kb = WINDOW ? attn_window_block(t, j) : t.w0 + j;
         const int kbase = kb * kAttnBlk;
         bool masked = (kbase + kAttnBlk > a.S) || (a.causal && kb == qblk);
         const int last = lastq - kbase;           // last visible key of the block
         [[maybe_unused]] uint32_t vis[4];         // WINDOW: the row's visible keys of a masked block
-        if constexpr (WINDOW) {
+        if constexpr (FORM == ATTN_WINDOW) {
           // the window of the tile's last row starts behind the block's first key, and not every key is a sink
           masked = masked || (qblk * kAttnBlk + kAttnBlk - a.window > kbase && a.nsink < kbase + kAttnBlk);
           if (masked)
@@ -893,7 +931,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
                        (~bits_below(last + 1 - a.window, 32 * k) | bits_below(a.nsink - kbase, 32 * k));
         }
         auto hidden = [&](int i) -> bool {
-          if constexpr (WINDOW) return !(vis[i >> 5] & (1u << (i & 31)));
+          if constexpr (FORM == ATTN_WINDOW) return !(vis[i >> 5] & (1u << (i & 31)));
           else return i > last;
         };
         // pass 1: the block's row max
@@ -974,6 +1012,31 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
         break;
       }
       tc_fence_after();
+      if constexpr (PREFIX) {
+        const long long part = (static_cast<long long>(t.seq) * a.tiles + qblk) * a.splits + t.split;
+        const bool valid = row < a.bpt * a.grp && qblk * a.bpt + row / a.grp < a.nseq;
+        float4* dst = reinterpret_cast<float4*>(a.parts + (part * 128 + row) * kAttnD);
+#pragma unroll 1
+        for (int cc = 0; cc < 8; ++cc) {
+          float v[16];
+          tmem_ld16(to + cc * 16, v);
+          if (valid) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              __stcg(dst + cc * 4 + i, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+          }
+        }
+        if (valid) {
+          __stcg(a.ml + part * 256 + row, m_ref * c);
+          __stcg(a.ml + part * 256 + 128 + row, l_run);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free(x));
+        cnt += nb;
+        ++its;
+        continue;
+      }
       const float inv = 1.0f / l_run;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
                            (static_cast<size_t>(t.seq) * a.S + qidx) * a.ldo + t.h * kAttnD;

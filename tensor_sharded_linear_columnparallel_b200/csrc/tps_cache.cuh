@@ -52,82 +52,695 @@ __global__ void __launch_bounds__(kAppendThreads) tps_kv_append_kernel(const KvA
   reinterpret_cast<uint4*>(cache + row * kAttnD)[chunk] = *src;
 }
 
-// ---------------------------------------------------------------- decode, plain form
-// One CTA per (sequence, KV head slot): it appends the token, then for each of the slot's
-// query heads its four warps walk the visible keys (a key per warp and step, a lane
-// holds four dimensions) with a running max and sum and meet in shared memory.
-constexpr int kDecThreads = 128;
+// ---------------------------------------------------------------- decode
+// One new token per sequence, G = qs / kvs query heads per KV head slot. The work is the
+// stream of the visible keys (512 bytes each), so it is cut by bytes: the 128-slot blocks
+// of all (sequence, KV head slot, chunk of 16 heads) items are numbered in one line and
+// every CTA (one per SM) takes an equal part of it, wherever that begins and ends. An item
+// cut by a border leaves its parts (running max, sum, unnormalised output, fp32) in the
+// workspace, and the CTA that finishes last merges them; its counter returns to zero.
+//
+// Blocks of 128 slots, with the roles of the two products exchanged so that the few heads
+// are the small side: S^T = K Q^T has M = 128 slots, N = 16 heads, K = 128 dimensions;
+// O^T += V^T P^T has M = 128 dimensions, N = 16 heads, K = 128 slots. Tensor memory holds
+// S^T twice and O^T twice (64 columns). Warp 0 loads K and V (three stages of 64 KB), warp
+// 1 issues the products, warps 2-5 hold one slot per thread for the softmax, warp 6 loads
+// the next item's queries and its new K and V rows ahead.
+//  - The new token's rows come from the QKV row itself: warp 6 writes them to the cache, and
+//    warp 1 puts them into the loaded block, so nothing waits for the write. Rows of V that
+//    the token does not see are zeroed there too: a slot never written may hold a NaN.
+//  - The reference max behind P moves only when a score exceeds it by more than 8 (base 2):
+//    one vote per block, and a reduction over the block only then (always at an item's
+//    first block). The weights are rounded to bf16 for the product, as in the prefill; the
+//    sum keeps them in fp32, a partial sum per thread until the item ends.
+constexpr int kDecThreads = 7 * 32;
+constexpr int kDecStages = 3;
+constexpr int kDecHeads = 16;                                     // heads per item
+constexpr int kDecStageBytes = 2 * kAttnTileBytes;                // K and V of one block
+constexpr int kDecOpBytes = kDecHeads * 256;                      // Q, or P: 16 rows of 128 bf16
+constexpr int kDecOffQ = kDecStages * kDecStageBytes;             // [2]
+constexpr int kDecOffP = kDecOffQ + 2 * kDecOpBytes;              // [2]
+constexpr int kDecOffNew = kDecOffP + 2 * kDecOpBytes;            // [2][K row, V row]
+constexpr int kDecOffRed = kDecOffNew + 2 * 512;                  // [4 warps][16] max, [4][16] sum, flags
+constexpr int kDecOffBar = kDecOffRed + 1024;
+constexpr int kDecSmemBytes = kDecOffBar + 256 + 1024;
+constexpr uint32_t kDecIdescS = idesc_bf16_f32(128, kDecHeads);
+constexpr uint32_t kDecIdescO = idesc_bf16_f32(128, kDecHeads) | (1u << 15);   // A (= V^T) MN-major
+static_assert(kDecSmemBytes <= 232448, "shared memory budget");
 
-__global__ void __launch_bounds__(kDecThreads) tps_decode_plain_kernel(const DecodeArgs a) {
-  __shared__ float sm[4], sl[4], so[4][kAttnD];
-  griddep_wait();
-  const int g = static_cast<int>(blockIdx.x) % a.nkv;
-  const int b = static_cast<int>(blockIdx.x) / a.nkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = g / a.kvs, lk = g - r * a.kvs;
-  const long long t = a.pos[b];
-  const bool live = t >= 0 && (a.linear == 0 || t < a.cap);
-  const __nv_bfloat16* row = a.qkv + static_cast<long long>(b) * a.ld + static_cast<long long>(r) * a.shard_cols;
-  __nv_bfloat16* kc = a.k + (static_cast<long long>(b) * a.nkv + g) * a.cap * kAttnD;
-  __nv_bfloat16* vc = a.v + (static_cast<long long>(b) * a.nkv + g) * a.cap * kAttnD;
-  if (live && threadIdx.x < 32) {
-    const int is_v = threadIdx.x >> 4, ch = threadIdx.x & 15;
-    const long long s = cache_slot(t, a.nsink, a.cap);
-    reinterpret_cast<uint4*>((is_v ? vc : kc) + s * kAttnD)[ch] =
-        reinterpret_cast<const uint4*>(row + (a.qs + is_v * a.kvs + lk) * kAttnD)[ch];
+// What the token at position t of a sequence sees, in slots: the sinks up to t, and the
+// `ring` newest positions behind them, whose newest has ring offset e. As blocks: [0, na)
+// and [nb0, nb1), no block in both.
+struct DecView {
+  int t, ring, e;
+  int slot;                    // the new token's own
+  int na, nb0, nb1;
+  __device__ __forceinline__ int blocks() const { return na + nb1 - nb0; }
+  __device__ __forceinline__ int block(int i) const { return i < na ? i : nb0 + i - na; }
+};
+
+__device__ __forceinline__ DecView dec_view(const DecodeArgs& a, int t) {
+  DecView v;
+  v.t = t;
+  v.slot = t;
+  v.ring = v.e = v.na = v.nb0 = v.nb1 = 0;
+  if (t < 0 || (a.linear && t >= a.cap)) return v;
+  if (t < a.nsink) {
+    v.na = (t >> 7) + 1;
+    return v;
   }
-  __syncthreads();
   const int R = a.cap - a.nsink;
-  const int G = a.qs / a.kvs;
-  const long long age0 = t >= a.nsink ? (t - a.nsink) % R : 0;   // ring offset of the newest token
-  for (int h = 0; h < G; ++h) {
-    const int hl = lk * G + h;
-    __nv_bfloat16* dst = a.out + static_cast<long long>(b) * a.ldo + (r * a.qs + hl) * kAttnD;
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f}, q[4];
-    for (int i = 0; i < 4; ++i) q[i] = __bfloat162float(row[hl * kAttnD + lane * 4 + i]);
-    const int P = a.prefix_len;
-    for (long long j = warp; live && j < static_cast<long long>(P) + a.cap; j += 4) {
-      const __nv_bfloat16 *kr, *vr;
-      if (j < P) {
-        kr = a.pk + (static_cast<long long>(g) * P + j) * kAttnD;
-        vr = a.pv + (static_cast<long long>(g) * P + j) * kAttnD;
-      } else {
-        const long long s = j - P;
-        bool see;
-        if (s < a.nsink) {
-          see = s <= t;
-        } else {
-          const long long age = (age0 - (s - a.nsink) + R) % R;
-          see = t >= a.nsink && age < a.window && t - age >= a.nsink;
-        }
-        if (!see) continue;
-        kr = kc + s * kAttnD;
-        vr = vc + s * kAttnD;
+  v.ring = min(t - a.nsink + 1, a.window);
+  v.e = (t - a.nsink) % R;
+  v.slot = a.nsink + v.e;
+  const int first = v.e - (v.ring - 1);                    // ring offset of the oldest, negative when wrapped
+  const int a_end = first >= 0 ? a.nsink : a.nsink + v.e + 1;
+  const int b_beg = first >= 0 ? a.nsink + first : a.nsink + first + R;
+  const int b_end = first >= 0 ? a.nsink + v.e + 1 : a.cap;
+  v.na = (a_end + 127) >> 7;
+  v.nb0 = max(b_beg >> 7, v.na);
+  v.nb1 = max((b_end + 127) >> 7, v.nb0);
+  return v;
+}
+
+__device__ __forceinline__ bool dec_sees(const DecodeArgs& a, const DecView& v, int slot) {
+  if (slot < a.nsink) return slot <= v.t;
+  int age = v.e - (slot - a.nsink);
+  if (age < 0) age += a.cap - a.nsink;
+  return slot < a.cap && age < v.ring;
+}
+
+// The part [w0, w1) of the line of blocks that a CTA works on, and the item it begins in.
+struct DecWork {
+  long long total, w0, w1;
+  int ctas;                    // CTAs with work (at most the grid, at most one per block)
+  int b;                       // first sequence
+  long long base;              // line index of that sequence's first block
+};
+
+__device__ __forceinline__ long long dec_border(const DecWork& w, int cta) { return w.total * cta / w.ctas; }
+// The CTA that works on block x of the line.
+__device__ __forceinline__ int dec_owner(const DecWork& w, long long x) {
+  return static_cast<int>(((x + 1) * w.ctas - 1) / w.total);
+}
+
+// One item as a CTA meets it: blocks [i0, i1) of its nb are this CTA's.
+struct DecItem {
+  int b, g, ch;                // sequence, KV head slot, chunk of 16 heads
+  int nb, i0, i1;
+  long long s;                 // line index of its first block
+  DecView v;
+};
+
+// Walks the items of a CTA's part in order; every role walks them by itself.
+struct DecWalk {
+  long long x, base;
+  int b;
+  DecView v;
+  __device__ __forceinline__ DecWalk(const DecodeArgs& a, const DecWork& w) : x(w.w0), base(w.base), b(w.b) {
+    if (x < w.w1) v = dec_view(a, __ldcg(a.pos + b));
+  }
+  __device__ __forceinline__ bool next(const DecodeArgs& a, const DecWork& w, DecItem& it) {
+    if (x >= w.w1) return false;
+    const int per = a.nkv * a.nch;
+    int nb = v.blocks();
+    while (x >= base + static_cast<long long>(per) * nb) {      // the next sequence with blocks
+      base += static_cast<long long>(per) * nb;
+      v = dec_view(a, __ldcg(a.pos + ++b));
+      nb = v.blocks();
+    }
+    const int k = static_cast<int>((x - base) / nb);
+    it.b = b;
+    it.g = k / a.nch;
+    it.ch = k - it.g * a.nch;
+    it.nb = nb;
+    it.s = base + static_cast<long long>(k) * nb;
+    it.i0 = static_cast<int>(x - it.s);
+    it.i1 = static_cast<int>(min(static_cast<long long>(nb), w.w1 - it.s));
+    it.v = v;
+    x = it.s + it.i1;
+    return true;
+  }
+};
+
+// Max (or sum) over the 32 lanes of 16 values per lane: lane l ends with the result of
+// value l >> 1 (both lanes of a pair the same): 8 + 4 + 2 + 1 exchanges, then one.
+template <bool MAX>
+__device__ __forceinline__ float warp_reduce16(const float (&x)[16], int lane) {
+  float v[8];
+  auto op = [](float p, float q) { return MAX ? fmaxf(p, q) : p + q; };
+  const bool h4 = lane & 16, h3 = lane & 8, h2 = lane & 4, h1 = lane & 2;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float keep = h4 ? x[8 + i] : x[i], give = h4 ? x[i] : x[8 + i];
+    v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, 16));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float keep = h3 ? v[4 + i] : v[i], give = h3 ? v[i] : v[4 + i];
+    v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, 8));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float keep = h2 ? v[2 + i] : v[i], give = h2 ? v[i] : v[2 + i];
+    v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, 4));
+  }
+  const float keep = h1 ? v[1] : v[0], give = h1 ? v[0] : v[1];
+  v[0] = op(keep, __shfl_xor_sync(0xffffffffu, give, 2));
+  return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+}
+
+__device__ __forceinline__ void dec_bar_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Barrier over the four softmax warps that returns whether any thread passed true.
+__device__ __forceinline__ bool dec_bar_or(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
+}
+
+// Byte offset of 16-byte chunk c (0..15) of row r of a [rows][128] bf16 tile held as two
+// boxes of [rows][64] with the 128-byte swizzle, `box` bytes apart.
+__device__ __forceinline__ uint32_t sw128_chunk(int r, int c, uint32_t box) {
+  return (c >> 3) * box + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ void fence_proxy_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Merges the parts of one item for head h with one warp (a lane holds four dimensions)
+// and writes the output row. part(c, o, m, l): addresses of part c.
+template <class Part>
+__device__ __forceinline__ void dec_merge(int n, int lane, Part part, __nv_bfloat16* dst) {
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = 0; c0 < n; c0 += 32) {
+    const int k = min(32, n - c0);
+    const float* o = nullptr;
+    float m = -INFINITY, l = 0.f;
+    if (lane < k) part(c0 + lane, o, m, l);
+    float mx = m;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+    const float Mn = fmaxf(M, mx);
+    const float sc = M == -INFINITY ? 0.f : ex2_approx(M - Mn);
+    const float f = m == -INFINITY ? 0.f : ex2_approx(m - Mn);
+    float fl = f * l;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) fl += __shfl_xor_sync(0xffffffffu, fl, x);
+    L = L * sc + fl;
+    M = Mn;
+    acc.x *= sc, acc.y *= sc, acc.z *= sc, acc.w *= sc;
+#pragma unroll 8
+    for (int i = 0; i < k; ++i) {
+      const float* p = reinterpret_cast<const float*>(
+          __shfl_sync(0xffffffffu, static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(o)), i));
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + lane);
+      acc.x = fmaf(fi, v.x, acc.x);
+      acc.y = fmaf(fi, v.y, acc.y);
+      acc.z = fmaf(fi, v.z, acc.z);
+      acc.w = fmaf(fi, v.w, acc.w);
+    }
+  }
+  const float inv = 1.0f / L;
+  reinterpret_cast<uint2*>(dst)[lane] = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+}
+
+__global__ void __launch_bounds__(kDecThreads, 1)
+    tps_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const DecodeArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t sBar = base + kDecOffBar;
+  auto kv_full = [&](int i) { return sBar + 8u * i; };            // [3] K and V of a block have landed
+  auto kv_empty = [&](int i) { return sBar + 24u + 8u * i; };     // [3]
+  auto s_full = [&](int i) { return sBar + 48u + 8u * i; };       // [2]
+  auto p_full = [&](int i) { return sBar + 64u + 8u * i; };       // [2]
+  auto q_full = [&](int i) { return sBar + 80u + 8u * i; };       // [2] by item
+  auto q_empty = [&](int i) { return sBar + 96u + 8u * i; };      // [2]
+  auto o_free = [&](int i) { return sBar + 112u + 8u * i; };      // [2] O^T of the item has been read
+  const uint32_t pv_done = sBar + 128u;                           // one phase per product with V
+  const uint32_t done_bar = sBar + 136u, epi_done_bar = sBar + 144u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kDecOffBar + 152);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + kDecOffBar + 156);
+  volatile int* never_flag = reinterpret_cast<volatile int*>(gbase + kDecOffBar + 160);
+  int* last_flag = reinterpret_cast<int*>(gbase + kDecOffBar + 164);
+  DecWork* sWork = reinterpret_cast<DecWork*>(gbase + kDecOffBar + 168);
+  static_assert(168 + sizeof(DecWork) <= 256, "barrier block");
+  long long* scan = reinterpret_cast<long long*>(gbase + kDecOffRed);   // [8] before the roles start
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kDecStages; ++i) {
+      mbar_init(kv_full(i), 1);
+      mbar_init(kv_empty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full(i), 1);
+      mbar_init(p_full(i), 4);
+      mbar_init(q_full(i), 1);
+      mbar_init(q_empty(i), 1);
+      mbar_init(o_free(i), 4);
+    }
+    mbar_init(pv_done, 1);
+    mbar_init(done_bar, 1);
+    mbar_init(epi_done_bar, 4);
+    *abort_flag = 0;
+    *never_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 64);
+    tmem_relinquish();
+  }
+  griddep_launch_dependents();
+  // Behind the prefix kernel this grid runs at the same time as that one, whose CTAs let it
+  // start only after they have waited for everything before them; what it reads before its
+  // own wait (the positions, the QKV rows, the caches) is older than both.
+  if (!a.prefix_parts) griddep_wait();
+  // the line of blocks: its length, then the sequence that this CTA's part begins in
+  {
+    const int per = a.nkv * a.nch;
+    long long sum = 0;
+    for (int b = threadIdx.x; b < a.nseq; b += kDecThreads) sum += dec_view(a, __ldcg(a.pos + b)).blocks();
+    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    if (lane == 0) scan[warp] = sum;
+    __syncthreads();
+    DecWork w;
+    w.total = 0;
+    for (int i = 0; i < kDecThreads / 32; ++i) w.total += scan[i];
+    w.total *= per;
+    w.ctas = static_cast<int>(min(w.total, static_cast<long long>(gridDim.x)));
+    const int cta = static_cast<int>(blockIdx.x);
+    w.w0 = w.w1 = 0;
+    w.b = 0;
+    w.base = 0;
+    if (cta < w.ctas) {
+      w.w0 = dec_border(w, cta);
+      w.w1 = dec_border(w, cta + 1);
+    }
+    if (threadIdx.x == 0) *sWork = w;
+    __syncthreads();                        // also: scan[] has been read
+    long long before = 0;
+    for (int b0 = 0; w.w0 < w.w1 && b0 < a.nseq; b0 += kDecThreads) {
+      const int b = b0 + threadIdx.x;
+      const long long n = b < a.nseq ? static_cast<long long>(per) * dec_view(a, __ldcg(a.pos + b)).blocks() : 0;
+      long long incl = n;
+      for (int x = 1; x < 32; x <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, x);
+        if (lane >= x) incl += y;
       }
-      float s = 0.f;
-      for (int i = 0; i < 4; ++i) s = fmaf(q[i], __bfloat162float(kr[lane * 4 + i]), s);
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      s *= a.scale_log2;
-      const float mn = fmaxf(m, s), al = exp2f(m - mn), p = exp2f(s - mn);
-      m = mn;
-      l = l * al + p;
-      for (int i = 0; i < 4; ++i) o[i] = o[i] * al + p * __bfloat162float(vr[lane * 4 + i]);
+      if (lane == 31) scan[warp] = incl;
+      __syncthreads();
+      long long excl = before + incl - n;
+      for (int i = 0; i < kDecThreads / 32; ++i) {
+        if (i < warp) excl += scan[i];
+        before += scan[i];
+      }
+      if (excl <= w.w0 && w.w0 < excl + n) {
+        sWork->b = b;
+        sWork->base = excl;
+      }
+      __syncthreads();
+      if (before > w.w0) break;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const DecWork w = *sWork;
+  const uint32_t tmem_base = *tmem_slot;
+  const uint64_t tmo = a.timeout_ns;
+  const int G = a.qs / a.kvs;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------ K and V of every block
+      long long n = 0;
+      bool ok = true;
+      DecWalk walk(a, w);
+      DecItem it;
+      while (ok && walk.next(a, w, it)) {
+        const int row = it.b * a.nkv + it.g;
+        for (int i = it.i0; i < it.i1; ++i, ++n) {
+          const int st = static_cast<int>(n % kDecStages);
+          if (!mbar_wait(kv_empty(st), static_cast<uint32_t>((n / kDecStages) & 1) ^ 1u, abort_flag, tmo, a.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = base + st * kDecStageBytes;
+          const int slot0 = it.v.block(i) * kAttnBlk;
+          mbar_arrive_expect_tx(kv_full(st), kDecStageBytes);
+          tma_load_3d(dst, &tmK, kv_full(st), 0, slot0, row);
+          tma_load_3d(dst + kAttnHalf, &tmK, kv_full(st), 64, slot0, row);
+          tma_load_3d(dst + kAttnTileBytes, &tmV, kv_full(st), 0, slot0, row);
+          tma_load_3d(dst + kAttnTileBytes + kAttnHalf, &tmV, kv_full(st), 64, slot0, row);
+        }
+      }
+      // wait (bounded) for the copies still in flight before the CTA may exit
+      for (long long i = n > kDecStages ? n - kDecStages : 0; i < n; ++i)
+        mbar_wait(kv_full(static_cast<int>(i % kDecStages)), static_cast<uint32_t>((i / kDecStages) & 1), never_flag,
+                  200000000ull, a.status);
+    }
+  } else if (warp == 6) {
+    // -------------------------------------------------- queries and new rows, one item ahead
+    int q = 0;
+    DecWalk walk(a, w);
+    DecItem it;
+    for (; walk.next(a, w, it); ++q) {
+      const int buf = q & 1;
+      const int r = it.g / a.kvs, lk = it.g - r * a.kvs;
+      const __nv_bfloat16* row =
+          a.qkv + static_cast<long long>(it.b) * a.ld + static_cast<long long>(r) * a.shard_cols;
+      const int h0 = it.ch * kDecHeads, gc = min(kDecHeads, G - h0);
+      uint4 x[8], kv;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {                    // 16 heads x 16 chunks over 32 lanes
+        const int h = 2 * i + (lane >> 4);
+        x[i] = h < gc ? __ldcg(reinterpret_cast<const uint4*>(row + (lk * G + h0 + h) * kAttnD) + (lane & 15))
+                      : make_uint4(0, 0, 0, 0);
+      }
+      const int is_v = lane >> 4;                      // lanes 0-15: the new K row, 16-31: the new V row
+      kv = __ldcg(reinterpret_cast<const uint4*>(row + (a.qs + is_v * a.kvs + lk) * kAttnD) + (lane & 15));
+      if (!__all_sync(0xffffffffu, mbar_wait(q_empty(buf), static_cast<uint32_t>((q >> 1) & 1) ^ 1u, abort_flag, tmo,
+                                             a.status)))
+        break;
+      const uint32_t sq = base + kDecOffQ + buf * kDecOpBytes;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        st_shared_v4(sq + sw128_chunk(2 * i + (lane >> 4), lane & 15, kDecOpBytes / 2), x[i].x, x[i].y, x[i].z, x[i].w);
+      st_shared_v4(base + kDecOffNew + buf * 512 + lane * 16, kv.x, kv.y, kv.z, kv.w);
+      const int slot = it.v.slot, sb = slot >> 7;
+      const int at_i = sb < it.v.na ? sb : sb - it.v.nb0 + it.v.na;   // the new slot's block, as one of the item's
+      if (at_i >= it.i0 && at_i < it.i1 && it.ch == 0) {
+        __nv_bfloat16* cache = is_v ? a.v : a.k;
+        const long long at = (static_cast<long long>(it.b) * a.nkv + it.g) * a.cap + slot;
+        reinterpret_cast<uint4*>(cache + at * kAttnD)[lane & 15] = kv;
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full(buf));
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------- products
+    long long n = 0;                                   // blocks of earlier items
+    int q = 0;
+    bool ok = true, any = false;
+    DecWalk walk(a, w);
+    DecItem it;
+    // the block is loaded: new rows in, unseen V rows out, then S^T = K Q^T
+    auto issue_s = [&](int i, long long nn) -> bool {
+      const int st = static_cast<int>(nn % kDecStages);
+      if (!__all_sync(0xffffffffu, mbar_wait(kv_full(st), static_cast<uint32_t>((nn / kDecStages) & 1), abort_flag,
+                                             tmo, a.status)))
+        return false;
+      const uint32_t kb = base + st * kDecStageBytes, vb = kb + kAttnTileBytes;
+      const int slot0 = it.v.block(i) * kAttnBlk;
+      bool touched = false;
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const int row = 32 * k + lane;
+        const bool see = dec_sees(a, it.v, slot0 + row);
+        if (!see) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {                // any order of a row's chunks: all become zero
+            st_shared_v4(vb + row * 128 + (((c + lane) & 7) << 4), 0, 0, 0, 0);
+            st_shared_v4(vb + kAttnHalf + row * 128 + (((c + lane) & 7) << 4), 0, 0, 0, 0);
+          }
+        }
+        touched |= __any_sync(0xffffffffu, !see);
+      }
+      const int nr = it.v.slot - slot0;
+      if (nr >= 0 && nr < kAttnBlk) {
+        const uint4 x = ld_shared_v4(base + kDecOffNew + (q & 1) * 512 + lane * 16);
+        st_shared_v4((lane < 16 ? kb : vb) + sw128_chunk(nr, lane & 15, kAttnHalf), x.x, x.y, x.z, x.w);
+        touched = true;
+      }
+      if (touched) fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        tc_fence_after();
+        const uint32_t sq = base + kDecOffQ + (q & 1) * kDecOpBytes;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint64_t off = static_cast<uint64_t>((kk & 3) * 2);   // 16 dimensions = 32 B along K
+          umma_bf16(tmem_base + static_cast<uint32_t>(nn & 1) * kDecHeads,
+                    smem_desc_sw128(kb + (kk < 4 ? 0 : kAttnHalf)) + off,
+                    smem_desc_sw128(sq + (kk < 4 ? 0 : kDecOpBytes / 2)) + off, kDecIdescS, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(s_full(static_cast<int>(nn & 1)));
+        if (i == it.i1 - 1) umma_commit(q_empty(q & 1));
+      }
+      __syncwarp();
+      return true;
+    };
+    for (; ok && walk.next(a, w, it); ++q) {
+      if (!__all_sync(0xffffffffu, mbar_wait(q_full(q & 1), static_cast<uint32_t>((q >> 1) & 1), abort_flag, tmo, a.status)) ||
+          !issue_s(it.i0, n)) {
+        ok = false;
+        break;
+      }
+      any = true;
+      for (int i = it.i0; i < it.i1; ++i, ++n) {
+        if (i + 1 < it.i1 && !issue_s(i + 1, n + 1)) { ok = false; break; }
+        const int st = static_cast<int>(n % kDecStages);
+        const int pb = static_cast<int>(n & 1);
+        // the first product of an item overwrites O^T of the item before the last
+        if (i == it.i0 && !__all_sync(0xffffffffu, mbar_wait(o_free(q & 1), static_cast<uint32_t>((q >> 1) & 1) ^ 1u,
+                                                             abort_flag, tmo, a.status))) {
+          ok = false;
+          break;
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(p_full(pb), static_cast<uint32_t>((n >> 1) & 1), abort_flag, tmo, a.status))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t vb = base + st * kDecStageBytes + kAttnTileBytes;
+          const uint32_t sp = base + kDecOffP + pb * kDecOpBytes;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)               // 16 slots per product: 2048 B of V, 32 B of P
+            umma_bf16(tmem_base + 32u + static_cast<uint32_t>(q & 1) * kDecHeads,
+                      smem_desc_sw128_mn(vb + kk * 2048, kAttnHalf),
+                      smem_desc_sw128(sp + (kk < 4 ? 0 : kDecOpBytes / 2)) + static_cast<uint64_t>((kk & 3) * 2),
+                      kDecIdescO, (i > it.i0 || kk > 0) ? 1u : 0u);
+          umma_commit(kv_empty(st));
+          umma_commit(pv_done);
+        }
+        __syncwarp();
+      }
     }
     if (lane == 0) {
-      sm[warp] = m;
-      sl[warp] = l;
+      // every issued product must be complete, and the softmax warps done, before tensor memory goes
+      if (any) {
+        umma_commit(done_bar);
+        mbar_wait(done_bar, 0, never_flag, 200000000ull, a.status);
+      }
+      mbar_wait(epi_done_bar, 0, never_flag, tmo, a.status);
     }
-    for (int i = 0; i < 4; ++i) so[warp][lane * 4 + i] = o[i];
-    __syncthreads();
-    const float mx = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float L = 0.f, O = 0.f;
-    for (int w = 0; w < 4; ++w) {
-      const float f = sm[w] == -INFINITY ? 0.f : exp2f(sm[w] - mx);
-      L += f * sl[w];
-      O += f * so[w][threadIdx.x];
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 64);
+  } else {
+    // -------------------------------------------------- softmax and output (warps 2-5)
+    // The four warps meet in named barriers, which cannot time out: a warp whose bounded
+    // wait failed keeps coming to them and reports there, and all four leave together.
+    const int q4 = warp & 3;                           // tensor-memory lane quarter
+    const int row = q4 * 32 + lane;                    // slot of a block; dimension of the output
+    const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+    float* red = reinterpret_cast<float*>(gbase + kDecOffRed);      // [4][16]
+    float* redl = red + 64;                                         // [4][16]
+    volatile int* flg = reinterpret_cast<volatile int*>(red + 128); // [4]
+    long long n = 0;
+    int q = 0;
+    bool ok = true;
+    DecWalk walk(a, w);
+    DecItem it;
+    for (; ok && walk.next(a, w, it); ++q) {
+      float mref[kDecHeads], lsum[kDecHeads];
+#pragma unroll
+      for (int h = 0; h < kDecHeads; ++h) {
+        mref[h] = -INFINITY;
+        lsum[h] = 0.f;
+      }
+      const uint32_t to = tmem_base + lane_off + 32u + static_cast<uint32_t>(q & 1) * kDecHeads;
+      for (int i = it.i0; i < it.i1; ++i, ++n) {
+        const int pb = static_cast<int>(n & 1);
+        if (ok)
+          ok = __all_sync(0xffffffffu, mbar_wait(s_full(pb), static_cast<uint32_t>((n >> 1) & 1), abort_flag, tmo, a.status));
+        float s[kDecHeads] = {};
+        bool move = !ok || i == it.i0;
+        if (ok) {
+          tc_fence_after();
+          tmem_ld16(tmem_base + lane_off + static_cast<uint32_t>(pb) * kDecHeads, s);
+          const bool see = dec_sees(a, it.v, it.v.block(i) * kAttnBlk + row);
+#pragma unroll
+          for (int h = 0; h < kDecHeads; ++h) {
+            s[h] = see ? s[h] * a.scale_log2 : -INFINITY;
+            move |= s[h] > mref[h] + 8.0f;
+          }
+        }
+        if (dec_bar_or(move)) {
+          const float mx = warp_reduce16<true>(s, lane);
+          if ((lane & 1) == 0) red[q4 * 16 + (lane >> 1)] = mx;
+          if (lane == 0) flg[q4] = ok ? 0 : 1;
+          dec_bar_sync();
+          if (flg[0] | flg[1] | flg[2] | flg[3]) {
+            ok = false;
+            break;
+          }
+          float al[kDecHeads];
+#pragma unroll
+          for (int h = 0; h < kDecHeads; ++h) {
+            const float mn = fmaxf(fmaxf(mref[h], fmaxf(red[h], red[16 + h])), fmaxf(red[32 + h], red[48 + h]));
+            al[h] = mn == -INFINITY ? 1.f : ex2_approx(mref[h] - mn);
+            mref[h] = mn;
+            lsum[h] *= al[h];
+          }
+          if (i > it.i0) {
+            // O^T must hold the products of every earlier block before it is scaled: all but the last
+            // are complete (S^T of this block was issued after them)
+            ok = __all_sync(0xffffffffu, mbar_wait(pv_done, static_cast<uint32_t>((n - 1) & 1), abort_flag, tmo, a.status));
+            if (ok) {
+              tc_fence_after();
+              float o[16];
+              tmem_ld16(to, o);
+#pragma unroll
+              for (int h = 0; h < kDecHeads; ++h) o[h] *= al[h];
+              tmem_st16_wait(to, o);
+            }
+          }
+          dec_bar_sync();                              // red[] is free again
+        }
+        if (ok) {
+          // P^T: this slot's column of the 16 x 128 tile
+          const uint32_t sp = base + kDecOffP + pb * kDecOpBytes + (row >> 6) * (kDecOpBytes / 2) + (row & 7) * 2;
+#pragma unroll
+          for (int h = 0; h < kDecHeads; ++h) {
+            const float p = ex2_approx(s[h] - (mref[h] == -INFINITY ? 0.f : mref[h]));
+            lsum[h] += p;
+            const __nv_bfloat16 pbf = __float2bfloat16_rn(p);
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(sp + h * 128 + ((((row & 63) >> 3) ^ (h & 7)) << 4)),
+                         "h"(*reinterpret_cast<const uint16_t*>(&pbf))
+                         : "memory");
+          }
+          fence_proxy_async_shared();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(pb));
+        }
+      }
+      // the item's part: products n-2 and n-1 may still run (the waits are in their order)
+      if (ok && n >= 2)
+        ok = __all_sync(0xffffffffu, mbar_wait(pv_done, static_cast<uint32_t>((n - 2) & 1), abort_flag, tmo, a.status));
+      if (ok)
+        ok = __all_sync(0xffffffffu, mbar_wait(pv_done, static_cast<uint32_t>((n - 1) & 1), abort_flag, tmo, a.status));
+      const float lw = warp_reduce16<false>(lsum, lane);
+      if ((lane & 1) == 0) redl[q4 * 16 + (lane >> 1)] = lw;
+      if (lane == 0) flg[q4] = ok ? 0 : 1;
+      dec_bar_sync();
+      if (flg[0] | flg[1] | flg[2] | flg[3]) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float o[16];
+      tmem_ld16(to, o);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free(q & 1));
+      const int r = it.g / a.kvs, lk = it.g - r * a.kvs;
+      const int h0 = it.ch * kDecHeads, gc = min(kDecHeads, G - h0);
+      const int hl = lk * G + h0;                      // first head of the item within its shard
+      __nv_bfloat16* dst = a.out + static_cast<long long>(it.b) * a.ldo + static_cast<long long>(r * a.qs + hl) * kAttnD;
+      const bool whole = it.i0 == 0 && it.i1 == it.nb;
+      if (whole && !a.prefix_parts) {
+#pragma unroll
+        for (int h = 0; h < kDecHeads; ++h)
+          if (h < gc) {
+            const float l = (redl[h] + redl[16 + h]) + (redl[32 + h] + redl[48 + h]);
+            dst[h * kAttnD + row] = __float2bfloat16_rn(o[h] / l);
+          }
+      } else {
+        // slot 0: the item that this CTA's part begins in, 1: the one it ends in, 2: a whole one
+        const int cta = static_cast<int>(blockIdx.x);
+        float* slot = a.parts + (static_cast<long long>(cta) * 3 + (whole ? 2 : it.s <= w.w0 ? 0 : 1)) * kDecPartFloats;
+#pragma unroll
+        for (int h = 0; h < kDecHeads; ++h)
+          if (h < gc) __stcg(slot + h * kAttnD + row, o[h]);
+#pragma unroll
+        for (int h = 0; h < kDecHeads; ++h)
+          if (row == h && h < gc) {
+            __stcg(slot + kDecHeads * kAttnD + h, mref[h]);
+            __stcg(slot + kDecHeads * kAttnD + kDecHeads + h, (redl[h] + redl[16 + h]) + (redl[32 + h] + redl[48 + h]));
+          }
+        const int c0 = whole ? cta : dec_owner(w, it.s), c1 = whole ? cta : dec_owner(w, it.s + it.nb - 1);
+        __threadfence();
+        dec_bar_sync();
+        if (!whole) {
+          const int item = (it.b * a.nkv + it.g) * a.nch + it.ch;
+          if (warp == 2 && lane == 0) {
+            const int old = atomicAdd(a.counters + item, 1);
+            *last_flag = old == c1 - c0;
+            if (old == c1 - c0) a.counters[item] = 0;  // left zero for the next call
+          }
+          dec_bar_sync();
+        }
+        if (whole || *last_flag) {
+          __threadfence();
+          if (a.prefix_parts) griddep_wait();          // the prefix kernel's parts are there
+          const int nw = c1 - c0 + 1;
+          const int n_parts = nw + (a.prefix_parts ? a.prefix_splits : 0);
+          for (int h = warp - 2; h < gc; h += 4) {
+            auto part = [&](int c, const float*& po, float& m, float& l) {
+              if (c < nw) {
+                const int cc = c0 + c;
+                const float* sl = a.parts + (static_cast<long long>(cc) * 3 +
+                                             (whole ? 2 : it.s <= dec_border(w, cc) ? 0 : 1)) * kDecPartFloats;
+                po = sl + h * kAttnD;
+                m = __ldcg(sl + kDecHeads * kAttnD + h);
+                l = __ldcg(sl + kDecHeads * kAttnD + kDecHeads + h);
+              } else {
+                const int per = 128 / G;               // sequences per tile of the prefix kernel
+                const long long pt =
+                    (static_cast<long long>(it.g) * a.prefix_tiles + it.b / per) * a.prefix_splits + (c - nw);
+                const int pr = (it.b % per) * G + h0 + h;
+                po = a.prefix_parts + (pt * 128 + pr) * kAttnD;
+                const float* ml = a.prefix_ml + pt * 256;
+                m = __ldcg(ml + pr);
+                l = __ldcg(ml + 128 + pr);
+              }
+            };
+            dec_merge(n_parts, lane, part, dst + h * kAttnD);
+          }
+        }
+        dec_bar_sync();                                // the flag and slot 2 are free again
+      }
     }
-    dst[threadIdx.x] = __float2bfloat16_rn(live ? O / L : 0.f);
-    __syncthreads();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(epi_done_bar);
+    // this grid must not complete before the prefix kernel, whichever items it had
+    if (a.prefix_parts) griddep_wait();
+    // unused rows of the batch
+    for (int b = blockIdx.x; b < a.nseq; b += gridDim.x)
+      if (dec_view(a, __ldcg(a.pos + b)).blocks() == 0)
+        for (int i = (warp - 2) * 32 + lane; i < a.ldo / 8; i += 128)
+          reinterpret_cast<uint4*>(a.out + static_cast<long long>(b) * a.ldo)[i] = make_uint4(0, 0, 0, 0);
   }
 }
 

@@ -99,6 +99,13 @@ struct AttnArgs {
   int ldo;                         // hq * d
   unsigned long long timeout_ns;
   int* status;                     // launch status word, or null (device-wide word only)
+  // PREFIX kernel: S is the prefix length; `grp` query heads per KV head slot; a tile is
+  // the rows of bpt sequences (row = sequence * grp + head); the key blocks of a KV head
+  // slot are cut into `splits` parts. Part p = (slot * tiles + tile) * splits + split:
+  // parts[p][128][128] (unnormalised output), ml[p][2][128] (reference max in log2 units,
+  // sum).
+  float *parts, *ml;
+  int nkv, bpt, tiles, splits;
 };
 
 // One append of a QKV output's K and V to the shards' caches (tps_cache.cuh).
@@ -122,12 +129,18 @@ struct DecodeArgs {
   int linear;                      // 1: position p is slot p, and pos >= cap is idle
   int window, nsink, cap;
   __nv_bfloat16 *k, *v;
-  const __nv_bfloat16 *pk, *pv;    // [nkv][prefix_len][128]
-  int prefix_len;
   float scale_log2;
   __nv_bfloat16* out;              // [nseq][ldo]
   int ldo;
+  int nch;                         // chunks of 16 query heads per KV head slot
+  int* counters;                   // [nseq*nkv*nch] CTAs that have left their part of an item, zero between calls
+  float* parts;                    // [grid][3][kDecPartFloats]: 16 x 128 output, 16 max, 16 sum
+  const float *prefix_parts, *prefix_ml;   // parts of the prefix kernel (see AttnArgs), or null
+  int prefix_tiles, prefix_splits;
+  unsigned long long timeout_ns;
+  int* status;
 };
+constexpr int kDecPartFloats = 16 * 128 + 32;
 
 // One sampling launch (tps_sample.cuh). The largest vocabulary is what eight CTAs hold in
 // shared memory as fp32.
@@ -209,7 +222,9 @@ int launch_attention(const CUtensorMap& tqkv, const AttnArgs& a, int two_tiles, 
 // sequence as its third dimension.
 int launch_window_attention(const CUtensorMap& tqkv, const AttnArgs& a, int grid, cudaStream_t st);
 int launch_kv_append(const KvAppendArgs& a, cudaStream_t st);
-int launch_decode(const DecodeArgs& a, cudaStream_t st);
+int launch_prefix_attention(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a,
+                            int grid, cudaStream_t st);
+int launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a, int grid, cudaStream_t st);
 int launch_sample(const SampleArgs& a, cudaStream_t st);
 int attention_smem_bytes(int two_tiles);
 // bf16_chain = 0: Y = P_0 + ... + P_{tp-1} (+ bias) in fp32; 1: every P_s rounded to

@@ -453,9 +453,10 @@ int launch_argmax_reduce(const void* part, int M, int tp, int per_shard_entries,
 
 int attention_smem_bytes(int two_tiles) { return two_tiles ? kAttn2SmemBytes : kAttnSmemBytes; }
 
-template <class Kernel>
-static int launch_attn_kernel(Kernel* fn, unsigned long long* attr_done, int threads, int smem,
-                              const CUtensorMap& tqkv, const AttnArgs& a, int grid, cudaStream_t st) {
+// Launches fn with its shared-memory opt-in (per device, remembered in *attr_done).
+template <class... P, class... Args>
+static int launch_with_smem(void (*fn)(P...), unsigned long long* attr_done, int threads, int smem, int grid,
+                            cudaStream_t st, const Args&... args) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return -6;
   const unsigned long long bit = 1ull << (dev & 63);
@@ -464,21 +465,28 @@ static int launch_attn_kernel(Kernel* fn, unsigned long long* attr_done, int thr
     __atomic_fetch_or(attr_done, bit, __ATOMIC_ACQ_REL);
   }
   LaunchCfg lc(grid, smem, st, 1, threads, true);
-  if (cudaLaunchKernelEx(&lc.cfg, fn, tqkv, a) != cudaSuccess) return -6;
+  if (cudaLaunchKernelEx(&lc.cfg, fn, args...) != cudaSuccess) return -6;
   return cudaGetLastError() == cudaSuccess ? 0 : -6;
 }
 
 int launch_attention(const CUtensorMap& tqkv, const AttnArgs& a, int two_tiles, int grid, cudaStream_t st) {
   static unsigned long long attr_done[2] = {0ull, 0ull};
-  return two_tiles ? launch_attn_kernel(tps_attn2_kernel<false>, &attr_done[1], kAttn2Threads, kAttn2SmemBytes, tqkv,
-                                        a, grid, st)
-                   : launch_attn_kernel(tps_attn_kernel, &attr_done[0], kAttnThreads, kAttnSmemBytes, tqkv, a, grid,
-                                        st);
+  return two_tiles ? launch_with_smem(tps_attn2_kernel<ATTN_FULL>, &attr_done[1], kAttn2Threads, kAttn2SmemBytes, grid,
+                                      st, tqkv, tqkv, tqkv, a)
+                   : launch_with_smem(tps_attn_kernel, &attr_done[0], kAttnThreads, kAttnSmemBytes, grid, st, tqkv, a);
 }
 
 int launch_window_attention(const CUtensorMap& tqkv, const AttnArgs& a, int grid, cudaStream_t st) {
   static unsigned long long attr_done = 0ull;
-  return launch_attn_kernel(tps_attn2_kernel<true>, &attr_done, kAttn2Threads, kAttn2SmemBytes, tqkv, a, grid, st);
+  return launch_with_smem(tps_attn2_kernel<ATTN_WINDOW>, &attr_done, kAttn2Threads, kAttn2SmemBytes, grid, st, tqkv,
+                          tqkv, tqkv, a);
+}
+
+int launch_prefix_attention(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a,
+                            int grid, cudaStream_t st) {
+  static unsigned long long attr_done = 0ull;
+  return launch_with_smem(tps_attn2_kernel<ATTN_PREFIX>, &attr_done, kAttn2Threads, kAttn2SmemBytes, grid, st, tq, tk,
+                          tv, a);
 }
 
 int launch_kv_append(const KvAppendArgs& a, cudaStream_t st) {
@@ -489,10 +497,9 @@ int launch_kv_append(const KvAppendArgs& a, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? 0 : -6;
 }
 
-int launch_decode(const DecodeArgs& a, cudaStream_t st) {
-  LaunchCfg lc(a.nseq * a.nkv, 0, st, 1, kDecThreads, true);
-  if (cudaLaunchKernelEx(&lc.cfg, tps_decode_plain_kernel, a) != cudaSuccess) return -6;
-  return cudaGetLastError() == cudaSuccess ? 0 : -6;
+int launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a, int grid, cudaStream_t st) {
+  static unsigned long long attr_done = 0ull;
+  return launch_with_smem(tps_decode_kernel, &attr_done, kDecThreads, kDecSmemBytes, grid, st, tk, tv, a);
 }
 
 int launch_sample(const SampleArgs& a, cudaStream_t st) {
