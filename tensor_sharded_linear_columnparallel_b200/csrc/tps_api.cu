@@ -1182,7 +1182,7 @@ int cache_geom(const tps_heads* heads, int tp, int64_t nsink, int64_t cap, HeadM
 struct DecodeWs {
   int nch;                      // chunks of 16 query heads per KV head slot
   int bpt, tiles, splits, nkb;  // prefix kernel: sequences per tile, tiles, parts of the key blocks
-  size_t counters, parts, ml, prefix_parts, bytes;
+  size_t counters, parts, item_parts, ml, prefix_parts, bytes;
 };
 
 DecodeWs decode_ws(int64_t nseq, const HeadMap& hm, int64_t nkv, int64_t prefix_len, int sms) {
@@ -1193,7 +1193,7 @@ DecodeWs decode_ws(int64_t nseq, const HeadMap& hm, int64_t nkv, int64_t prefix_
   w.counters = at;
   at += round256(static_cast<size_t>(nseq) * nkv * w.nch * 4);
   w.parts = at;
-  at += round256(static_cast<size_t>(sms) * 3 * tps::kDecPartFloats * 4);
+  at += round256(static_cast<size_t>(sms) * 2 * tps::kDecPartFloats * 4);
   if (prefix_len > 0 && G <= 128) {
     w.bpt = 128 / G;
     w.tiles = static_cast<int>((nseq + w.bpt - 1) / w.bpt);
@@ -1211,6 +1211,8 @@ DecodeWs decode_ws(int64_t nseq, const HeadMap& hm, int64_t nkv, int64_t prefix_
       }
     }
     const size_t np = static_cast<size_t>(nkv) * w.tiles * w.splits;
+    w.item_parts = at;
+    at += round256(static_cast<size_t>(nseq) * nkv * w.nch * tps::kDecPartFloats * 4);
     w.ml = at;
     at += np * 256 * 4;
     w.prefix_parts = at;
@@ -1234,6 +1236,8 @@ int run_decode(const void* qkv, int64_t nseq, const tps_heads* heads, const Head
   if (!aligned16(qkv) || !aligned4(pos) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(attn_out) ||
       !aligned16(ws))
     return TPS_ERR_ALIGN;
+  const int64_t blocks = nseq * nkv * ((hm.qs / hm.kvs + 15) / 16) * ((cap + 127) / 128);   // at most
+  if (blocks > 0x7fffffffLL) return TPS_ERR_ARG;
   const int sms = num_sms_current();
   const DecodeWs lay = decode_ws(nseq, hm, nkv, prefix_len, sms);
   if (ws_bytes < lay.bytes) return TPS_ERR_WORKSPACE;
@@ -1295,12 +1299,12 @@ int run_decode(const void* qkv, int64_t nseq, const tps_heads* heads, const Head
     if (rc == TPS_OK) rc = make_map(&tpv, prefix_v, d, P, static_cast<uint64_t>(nkv), row, row * P, 128, 1);
     if (rc) return rc;
     if (tps::launch_prefix_attention(tq, tpk, tpv, p, p.items < sms ? p.items : sms, st) != 0) return TPS_ERR_CUDA;
+    a->item_parts = reinterpret_cast<float*>(wsp + lay.item_parts);
     a->prefix_parts = p.parts;
     a->prefix_ml = p.ml;
     a->prefix_tiles = lay.tiles;
     a->prefix_splits = lay.splits;
   }
-  const int64_t blocks = nseq * nkv * lay.nch * ((cap + 127) / 128);   // at most
   return tps::launch_decode(tk, tv, *a, static_cast<int>(std::min<int64_t>(blocks, sms)), st) == 0 ? TPS_OK
                                                                                                   : TPS_ERR_CUDA;
 }

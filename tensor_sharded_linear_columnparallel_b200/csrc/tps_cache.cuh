@@ -59,6 +59,10 @@ __global__ void __launch_bounds__(kAppendThreads) tps_kv_append_kernel(const KvA
 // every CTA (one per SM) takes an equal part of it, wherever that begins and ends. An item
 // cut by a border leaves its parts (running max, sum, unnormalised output, fp32) in the
 // workspace, and the CTA that finishes last merges them; its counter returns to zero.
+// Behind a shared prefix every item leaves a part, to be merged with the prefix kernel's.
+// Merging waits until the CTA's stream has ended and then uses all its warps, one output
+// row each: done where an item ends, it held the stream up (window_decode of 32 sequences
+// with 4100 visible keys: 96 us; 64 sequences behind a prefix of 16384: 118 us).
 //
 // Blocks of 128 slots, with the roles of the two products exchanged so that the few heads
 // are the small side: S^T = K Q^T has M = 128 slots, N = 16 heads, K = 128 dimensions;
@@ -130,58 +134,74 @@ __device__ __forceinline__ bool dec_sees(const DecodeArgs& a, const DecView& v, 
   return slot < a.cap && age < v.ring;
 }
 
-// The part [w0, w1) of the line of blocks that a CTA works on, and the item it begins in.
+// The line of blocks of all items (sequence, then KV head slot, then chunk), and the part
+// [w0, w1) of it that this CTA works on: the first `rem` CTAs take share + 1 blocks, the
+// others share. It has fewer than 2^31 blocks (the host checks: 2^31 blocks are 128 TB).
 struct DecWork {
-  long long total, w0, w1;
-  int ctas;                    // CTAs with work (at most the grid, at most one per block)
-  int b;                       // first sequence
-  long long base;              // line index of that sequence's first block
+  int ctas, share, rem;        // CTAs with work (at most the grid, at most one per block)
+  int w0, w1;
+  int b, t;                    // the sequence that w0 lies in, its token's position
+  int base;                    // line index of that sequence's first block
 };
 
-__device__ __forceinline__ long long dec_border(const DecWork& w, int cta) { return w.total * cta / w.ctas; }
+__device__ __forceinline__ int dec_border(const DecWork& w, int cta) { return cta * w.share + min(cta, w.rem); }
 // The CTA that works on block x of the line.
-__device__ __forceinline__ int dec_owner(const DecWork& w, long long x) {
-  return static_cast<int>(((x + 1) * w.ctas - 1) / w.total);
+__device__ __forceinline__ int dec_owner(const DecWork& w, int x) {
+  const int head = w.rem * (w.share + 1);
+  return x < head ? x / (w.share + 1) : w.rem + (x - head) / w.share;
 }
 
 // One item as a CTA meets it: blocks [i0, i1) of its nb are this CTA's.
 struct DecItem {
   int b, g, ch;                // sequence, KV head slot, chunk of 16 heads
   int nb, i0, i1;
-  long long s;                 // line index of its first block
+  int s;                       // line index of its first block
   DecView v;
+  __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == nb; }
 };
 
 // Walks the items of a CTA's part in order; every role walks them by itself.
 struct DecWalk {
-  long long x, base;
-  int b;
+  int x, b, k, tnext;          // next block; its sequence; item within the sequence; position of sequence b + 1
   DecView v;
-  __device__ __forceinline__ DecWalk(const DecodeArgs& a, const DecWork& w) : x(w.w0), base(w.base), b(w.b) {
-    if (x < w.w1) v = dec_view(a, __ldcg(a.pos + b));
+  __device__ __forceinline__ DecWalk(const DecodeArgs& a, const DecWork& w) : x(w.w0), b(w.b), k(0) {
+    v = dec_view(a, w.t);
+    tnext = b + 1 < a.nseq ? __ldcg(a.pos + b + 1) : -1;
+    if (w.w0 < w.w1) k = (w.w0 - w.base) / v.blocks();
+    s = w.base + k * v.blocks();
   }
   __device__ __forceinline__ bool next(const DecodeArgs& a, const DecWork& w, DecItem& it) {
     if (x >= w.w1) return false;
-    const int per = a.nkv * a.nch;
-    int nb = v.blocks();
-    while (x >= base + static_cast<long long>(per) * nb) {      // the next sequence with blocks
-      base += static_cast<long long>(per) * nb;
-      v = dec_view(a, __ldcg(a.pos + ++b));
-      nb = v.blocks();
+    while (k == a.nkv * a.nch || v.blocks() == 0) {             // the next sequence with blocks
+      v = dec_view(a, tnext);
+      ++b;
+      tnext = b + 1 < a.nseq ? __ldcg(a.pos + b + 1) : -1;
+      k = 0;
     }
-    const int k = static_cast<int>((x - base) / nb);
     it.b = b;
-    it.g = k / a.nch;
+    it.g = a.nch == 1 ? k : k / a.nch;
     it.ch = k - it.g * a.nch;
-    it.nb = nb;
-    it.s = base + static_cast<long long>(k) * nb;
-    it.i0 = static_cast<int>(x - it.s);
-    it.i1 = static_cast<int>(min(static_cast<long long>(nb), w.w1 - it.s));
+    it.nb = v.blocks();
+    it.s = s;
+    it.i0 = x - s;
+    it.i1 = min(it.nb, w.w1 - s);
     it.v = v;
+    s += it.nb;
     x = it.s + it.i1;
+    ++k;
     return true;
   }
+
+ private:
+  int s;                       // line index of item k
 };
+
+// Where CTA cta leaves its part of an item: per item where it has the whole of it (behind a
+// prefix), else per CTA, which cuts at most the item that it begins in and the one it ends in.
+__device__ __forceinline__ float* dec_part(const DecodeArgs& a, const DecWork& w, const DecItem& it, int cta) {
+  if (it.whole()) return a.item_parts + (static_cast<long long>(it.b * a.nkv + it.g) * a.nch + it.ch) * kDecPartFloats;
+  return a.parts + (static_cast<long long>(cta) * 2 + (it.s <= dec_border(w, cta) ? 0 : 1)) * kDecPartFloats;
+}
 
 // Max (or sum) over the 32 lanes of 16 values per lane: lane l ends with the result of
 // value l >> 1 (both lanes of a pair the same): 8 + 4 + 2 + 1 exchanges, then one.
@@ -235,17 +255,26 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Merges the parts of one item for head h with one warp (a lane holds four dimensions)
-// and writes the output row. part(c, o, m, l): addresses of part c.
+// Merges the n parts of one output row with one warp, a lane holding four dimensions.
+// part(c): the address of part c's 128 outputs, with its max and sum in m and l. The
+// loads of 20 parts are in flight before the first is used.
 template <class Part>
 __device__ __forceinline__ void dec_merge(int n, int lane, Part part, __nv_bfloat16* dst) {
   float M = -INFINITY, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c0 = 0; c0 < n; c0 += 32) {
-    const int k = min(32, n - c0);
+  constexpr int kIn = 20;
+  for (int c0 = 0; c0 < n; c0 += kIn) {
+    const int k = min(kIn, n - c0);
     const float* o = nullptr;
     float m = -INFINITY, l = 0.f;
-    if (lane < k) part(c0 + lane, o, m, l);
+    if (lane < k) o = part(c0 + lane, m, l);
+    float4 v[kIn];
+#pragma unroll
+    for (int i = 0; i < kIn; ++i) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<uintptr_t>(
+          __shfl_sync(0xffffffffu, static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(o)), i)));
+      v[i] = i < k ? __ldcg(p + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     float mx = m;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
@@ -258,16 +287,13 @@ __device__ __forceinline__ void dec_merge(int n, int lane, Part part, __nv_bfloa
     L = L * sc + fl;
     M = Mn;
     acc.x *= sc, acc.y *= sc, acc.z *= sc, acc.w *= sc;
-#pragma unroll 8
-    for (int i = 0; i < k; ++i) {
-      const float* p = reinterpret_cast<const float*>(
-          __shfl_sync(0xffffffffu, static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(o)), i));
+#pragma unroll
+    for (int i = 0; i < kIn; ++i) {
       const float fi = __shfl_sync(0xffffffffu, f, i);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + lane);
-      acc.x = fmaf(fi, v.x, acc.x);
-      acc.y = fmaf(fi, v.y, acc.y);
-      acc.z = fmaf(fi, v.z, acc.z);
-      acc.w = fmaf(fi, v.w, acc.w);
+      acc.x = fmaf(fi, v[i].x, acc.x);
+      acc.y = fmaf(fi, v[i].y, acc.y);
+      acc.z = fmaf(fi, v[i].z, acc.z);
+      acc.w = fmaf(fi, v[i].w, acc.w);
     }
   }
   const float inv = 1.0f / L;
@@ -289,15 +315,17 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   auto q_full = [&](int i) { return sBar + 80u + 8u * i; };       // [2] by item
   auto q_empty = [&](int i) { return sBar + 96u + 8u * i; };      // [2]
   auto o_free = [&](int i) { return sBar + 112u + 8u * i; };      // [2] O^T of the item has been read
-  const uint32_t pv_done = sBar + 128u;                           // one phase per product with V
-  const uint32_t done_bar = sBar + 136u, epi_done_bar = sBar + 144u;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kDecOffBar + 152);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + kDecOffBar + 156);
-  volatile int* never_flag = reinterpret_cast<volatile int*>(gbase + kDecOffBar + 160);
-  int* last_flag = reinterpret_cast<int*>(gbase + kDecOffBar + 164);
-  DecWork* sWork = reinterpret_cast<DecWork*>(gbase + kDecOffBar + 168);
-  static_assert(168 + sizeof(DecWork) <= 256, "barrier block");
-  long long* scan = reinterpret_cast<long long*>(gbase + kDecOffRed);   // [8] before the roles start
+  // Product n with V completes a phase of barrier n & 1. A wait for product k is exact: k + 2
+  // cannot complete before the waiting warps have gone on, and k - 2 has completed before.
+  auto pv_done = [&](int i) { return sBar + 128u + 8u * i; };     // [2]
+  const uint32_t done_bar = sBar + 144u, epi_done_bar = sBar + 152u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kDecOffBar + 160);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + kDecOffBar + 164);
+  volatile int* never_flag = reinterpret_cast<volatile int*>(gbase + kDecOffBar + 168);
+  int* last_flag = reinterpret_cast<int*>(gbase + kDecOffBar + 172);    // [4]: cut items, their other CTAs
+  DecWork* sWork = reinterpret_cast<DecWork*>(gbase + kDecOffBar + 192);
+  static_assert(192 + sizeof(DecWork) <= 256, "barrier block");
+  int* scan = reinterpret_cast<int*>(gbase + kDecOffRed);   // [8] before the roles start
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -312,12 +340,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       mbar_init(q_full(i), 1);
       mbar_init(q_empty(i), 1);
       mbar_init(o_free(i), 4);
+      mbar_init(pv_done(i), 1);
     }
-    mbar_init(pv_done, 1);
     mbar_init(done_bar, 1);
     mbar_init(epi_done_bar, 4);
     *abort_flag = 0;
     *never_flag = 0;
+    last_flag[0] = last_flag[1] = -1;
     fence_mbar_init();
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -334,46 +363,63 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   // the line of blocks: its length, then the sequence that this CTA's part begins in
   {
     const int per = a.nkv * a.nch;
-    long long sum = 0;
-    for (int b = threadIdx.x; b < a.nseq; b += kDecThreads) sum += dec_view(a, __ldcg(a.pos + b)).blocks();
-    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    if (lane == 0) scan[warp] = sum;
+    const int t0 = threadIdx.x < a.nseq ? __ldcg(a.pos + threadIdx.x) : -1;
+    const int n0 = per * dec_view(a, t0).blocks();
+    int sum = n0;
+    for (int b = threadIdx.x + kDecThreads; b < a.nseq; b += kDecThreads)
+      sum += per * dec_view(a, __ldcg(a.pos + b)).blocks();
+    int incl = sum;                         // with one sequence per thread, also the scan below
+    for (int x = 1; x < 32; x <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, x);
+      if (lane >= x) incl += y;
+    }
+    if (lane == 31) scan[warp] = incl;
     __syncthreads();
+    int total = 0, excl = incl - sum;
+    for (int i = 0; i < kDecThreads / 32; ++i) {
+      if (i < warp) excl += scan[i];
+      total += scan[i];
+    }
     DecWork w;
-    w.total = 0;
-    for (int i = 0; i < kDecThreads / 32; ++i) w.total += scan[i];
-    w.total *= per;
-    w.ctas = static_cast<int>(min(w.total, static_cast<long long>(gridDim.x)));
+    w.ctas = min(total, static_cast<int>(gridDim.x));
+    w.share = w.ctas ? total / w.ctas : 0;
+    w.rem = total - w.share * w.ctas;
     const int cta = static_cast<int>(blockIdx.x);
-    w.w0 = w.w1 = 0;
-    w.b = 0;
-    w.base = 0;
+    w.w0 = w.w1 = w.b = w.t = w.base = 0;
     if (cta < w.ctas) {
       w.w0 = dec_border(w, cta);
       w.w1 = dec_border(w, cta + 1);
     }
     if (threadIdx.x == 0) *sWork = w;
     __syncthreads();                        // also: scan[] has been read
-    long long before = 0;
+    int before = 0;
     for (int b0 = 0; w.w0 < w.w1 && b0 < a.nseq; b0 += kDecThreads) {
       const int b = b0 + threadIdx.x;
-      const long long n = b < a.nseq ? static_cast<long long>(per) * dec_view(a, __ldcg(a.pos + b)).blocks() : 0;
-      long long incl = n;
-      for (int x = 1; x < 32; x <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, x);
-        if (lane >= x) incl += y;
-      }
-      if (lane == 31) scan[warp] = incl;
-      __syncthreads();
-      long long excl = before + incl - n;
-      for (int i = 0; i < kDecThreads / 32; ++i) {
-        if (i < warp) excl += scan[i];
-        before += scan[i];
+      int t = t0, n = n0;
+      if (a.nseq > kDecThreads) {
+        if (b0 > 0) {
+          t = b < a.nseq ? __ldcg(a.pos + b) : -1;
+          n = per * dec_view(a, t).blocks();
+        }
+        incl = n;
+        for (int x = 1; x < 32; x <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, x);
+          if (lane >= x) incl += y;
+        }
+        if (lane == 31) scan[warp] = incl;
+        __syncthreads();
+        excl = before + incl - n;
+        for (int i = 0; i < kDecThreads / 32; ++i) {
+          if (i < warp) excl += scan[i];
+          before += scan[i];
+        }
       }
       if (excl <= w.w0 && w.w0 < excl + n) {
         sWork->b = b;
+        sWork->t = t;
         sWork->base = excl;
       }
+      if (a.nseq <= kDecThreads) break;
       __syncthreads();
       if (before > w.w0) break;
     }
@@ -539,7 +585,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                       smem_desc_sw128(sp + (kk < 4 ? 0 : kDecOpBytes / 2)) + static_cast<uint64_t>((kk & 3) * 2),
                       kDecIdescO, (i > it.i0 || kk > 0) ? 1u : 0u);
           umma_commit(kv_empty(st));
-          umma_commit(pv_done);
+          umma_commit(pv_done(pb));
         }
         __syncwarp();
       }
@@ -614,7 +660,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           if (i > it.i0) {
             // O^T must hold the products of every earlier block before it is scaled: all but the last
             // are complete (S^T of this block was issued after them)
-            ok = __all_sync(0xffffffffu, mbar_wait(pv_done, static_cast<uint32_t>((n - 1) & 1), abort_flag, tmo, a.status));
+            ok = __all_sync(0xffffffffu, mbar_wait(pv_done(pb ^ 1), static_cast<uint32_t>(((n - 1) >> 1) & 1), abort_flag,
+                                                        tmo, a.status));
             if (ok) {
               tc_fence_after();
               float o[16];
@@ -644,11 +691,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           if (lane == 0) mbar_arrive(p_full(pb));
         }
       }
-      // the item's part: products n-2 and n-1 may still run (the waits are in their order)
-      if (ok && n >= 2)
-        ok = __all_sync(0xffffffffu, mbar_wait(pv_done, static_cast<uint32_t>((n - 2) & 1), abort_flag, tmo, a.status));
-      if (ok)
-        ok = __all_sync(0xffffffffu, mbar_wait(pv_done, static_cast<uint32_t>((n - 1) & 1), abort_flag, tmo, a.status));
+      if (ok)                                          // the item's last product
+        ok = __all_sync(0xffffffffu, mbar_wait(pv_done(static_cast<int>((n - 1) & 1)),
+                                               static_cast<uint32_t>(((n - 1) >> 1) & 1), abort_flag, tmo, a.status));
       const float lw = warp_reduce16<false>(lsum, lane);
       if ((lane & 1) == 0) redl[q4 * 16 + (lane >> 1)] = lw;
       if (lane == 0) flg[q4] = ok ? 0 : 1;
@@ -667,8 +712,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const int h0 = it.ch * kDecHeads, gc = min(kDecHeads, G - h0);
       const int hl = lk * G + h0;                      // first head of the item within its shard
       __nv_bfloat16* dst = a.out + static_cast<long long>(it.b) * a.ldo + static_cast<long long>(r * a.qs + hl) * kAttnD;
-      const bool whole = it.i0 == 0 && it.i1 == it.nb;
-      if (whole && !a.prefix_parts) {
+      if (it.whole() && !a.prefix_parts) {
 #pragma unroll
         for (int h = 0; h < kDecHeads; ++h)
           if (h < gc) {
@@ -676,72 +720,86 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             dst[h * kAttnD + row] = __float2bfloat16_rn(o[h] / l);
           }
       } else {
-        // slot 0: the item that this CTA's part begins in, 1: the one it ends in, 2: a whole one
-        const int cta = static_cast<int>(blockIdx.x);
-        float* slot = a.parts + (static_cast<long long>(cta) * 3 + (whole ? 2 : it.s <= w.w0 ? 0 : 1)) * kDecPartFloats;
+        float* slot = dec_part(a, w, it, static_cast<int>(blockIdx.x));
+        if (!it.whole() && warp == 2 && lane == 0) {   // counted below, when the part is written
+          const int k = it.s <= w.w0 ? 0 : 1;
+          last_flag[k] = (it.b * a.nkv + it.g) * a.nch + it.ch;
+          last_flag[2 + k] = dec_owner(w, it.s + it.nb - 1) - dec_owner(w, it.s);
+        }
 #pragma unroll
         for (int h = 0; h < kDecHeads; ++h)
-          if (h < gc) __stcg(slot + h * kAttnD + row, o[h]);
-#pragma unroll
-        for (int h = 0; h < kDecHeads; ++h)
-          if (row == h && h < gc) {
-            __stcg(slot + kDecHeads * kAttnD + h, mref[h]);
-            __stcg(slot + kDecHeads * kAttnD + kDecHeads + h, (redl[h] + redl[16 + h]) + (redl[32 + h] + redl[48 + h]));
+          if (h < gc) {
+            __stcg(slot + h * kAttnD + row, o[h]);
+            if (row == h) {
+              __stcg(slot + kDecHeads * kAttnD + h, mref[h]);
+              __stcg(slot + kDecHeads * kAttnD + kDecHeads + h,
+                     (redl[h] + redl[16 + h]) + (redl[32 + h] + redl[48 + h]));
+            }
           }
-        const int c0 = whole ? cta : dec_owner(w, it.s), c1 = whole ? cta : dec_owner(w, it.s + it.nb - 1);
-        __threadfence();
-        dec_bar_sync();
-        if (!whole) {
-          const int item = (it.b * a.nkv + it.g) * a.nch + it.ch;
-          if (warp == 2 && lane == 0) {
-            const int old = atomicAdd(a.counters + item, 1);
-            *last_flag = old == c1 - c0;
-            if (old == c1 - c0) a.counters[item] = 0;  // left zero for the next call
-          }
-          dec_bar_sync();
-        }
-        if (whole || *last_flag) {
-          __threadfence();
-          if (a.prefix_parts) griddep_wait();          // the prefix kernel's parts are there
-          const int nw = c1 - c0 + 1;
-          const int n_parts = nw + (a.prefix_parts ? a.prefix_splits : 0);
-          for (int h = warp - 2; h < gc; h += 4) {
-            auto part = [&](int c, const float*& po, float& m, float& l) {
-              if (c < nw) {
-                const int cc = c0 + c;
-                const float* sl = a.parts + (static_cast<long long>(cc) * 3 +
-                                             (whole ? 2 : it.s <= dec_border(w, cc) ? 0 : 1)) * kDecPartFloats;
-                po = sl + h * kAttnD;
-                m = __ldcg(sl + kDecHeads * kAttnD + h);
-                l = __ldcg(sl + kDecHeads * kAttnD + kDecHeads + h);
-              } else {
-                const int per = 128 / G;               // sequences per tile of the prefix kernel
-                const long long pt =
-                    (static_cast<long long>(it.g) * a.prefix_tiles + it.b / per) * a.prefix_splits + (c - nw);
-                const int pr = (it.b % per) * G + h0 + h;
-                po = a.prefix_parts + (pt * 128 + pr) * kAttnD;
-                const float* ml = a.prefix_ml + pt * 256;
-                m = __ldcg(ml + pr);
-                l = __ldcg(ml + 128 + pr);
-              }
-            };
-            dec_merge(n_parts, lane, part, dst + h * kAttnD);
-          }
-        }
-        dec_bar_sync();                                // the flag and slot 2 are free again
       }
     }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(epi_done_bar);
-    // this grid must not complete before the prefix kernel, whichever items it had
-    if (a.prefix_parts) griddep_wait();
-    // unused rows of the batch
-    for (int b = blockIdx.x; b < a.nseq; b += gridDim.x)
-      if (dec_view(a, __ldcg(a.pos + b)).blocks() == 0)
-        for (int i = (warp - 2) * 32 + lane; i < a.ldo / 8; i += 128)
-          reinterpret_cast<uint4*>(a.out + static_cast<long long>(b) * a.ldo)[i] = make_uint4(0, 0, 0, 0);
   }
+
+  // ---------------------------------------------------- merging and unused rows, all warps
+  __threadfence();
+  __syncthreads();                                     // every role is done, this CTA's parts are written
+  // also: this grid must not complete before the prefix kernel, whichever items it had
+  if (a.prefix_parts) griddep_wait();
+  const int cta = static_cast<int>(blockIdx.x);
+  if (!*abort_flag && w.w0 < w.w1) {
+    // the cut items are this CTA's first and last: two threads count them, and put 1 where
+    // the last of an item's CTAs is this one
+    if (lane == 0 && warp < 2) {
+      const int item = last_flag[warp];
+      bool last = false;
+      if (item >= 0) {
+        last = atomicAdd(a.counters + item, 1) == last_flag[2 + warp];
+        if (last) a.counters[item] = 0;                // left zero for the next call
+      }
+      __threadfence();
+      last_flag[warp] = last;
+    }
+    __syncthreads();
+    int job = 0;
+    DecWalk walk(a, w);
+    DecItem it;
+    while (walk.next(a, w, it)) {
+      const bool whole = it.whole();
+      if (whole ? !a.prefix_parts : !last_flag[it.s <= w.w0 ? 0 : 1]) continue;
+      const int r = it.g / a.kvs, lk = it.g - r * a.kvs;
+      const int h0 = it.ch * kDecHeads, gc = min(kDecHeads, G - h0);
+      const int c0 = whole ? cta : dec_owner(w, it.s);
+      const int nw = whole ? 1 : dec_owner(w, it.s + it.nb - 1) - c0 + 1;
+      for (int h = 0; h < gc; ++h, ++job) {
+        if (job % (kDecThreads / 32) != warp) continue;
+        auto part = [&](int c, float& m, float& l) -> const float* {
+          if (c < nw) {
+            const float* sl = dec_part(a, w, it, c0 + c);
+            m = __ldcg(sl + kDecHeads * kAttnD + h);
+            l = __ldcg(sl + kDecHeads * kAttnD + kDecHeads + h);
+            return sl + h * kAttnD;
+          }
+          const int per = 128 / G;                     // sequences per tile of the prefix kernel
+          const long long pt =
+              (static_cast<long long>(it.g) * a.prefix_tiles + it.b / per) * a.prefix_splits + (c - nw);
+          const int pr = (it.b % per) * G + h0 + h;
+          m = __ldcg(a.prefix_ml + pt * 256 + pr);
+          l = __ldcg(a.prefix_ml + pt * 256 + 128 + pr);
+          return a.prefix_parts + (pt * 128 + pr) * kAttnD;
+        };
+        dec_merge(nw + (a.prefix_parts ? a.prefix_splits : 0), lane, part,
+                  a.out + static_cast<long long>(it.b) * a.ldo +
+                      static_cast<long long>(r * a.qs + lk * G + h0 + h) * kAttnD);
+      }
+    }
+  }
+  for (int b = cta; b < a.nseq; b += gridDim.x)
+    if (dec_view(a, __ldcg(a.pos + b)).blocks() == 0)
+      for (int i = threadIdx.x; i < a.ldo / 8; i += kDecThreads)
+        reinterpret_cast<uint4*>(a.out + static_cast<long long>(b) * a.ldo)[i] = make_uint4(0, 0, 0, 0);
 }
 
 }  // namespace tps

@@ -134,7 +134,8 @@ struct DecodeArgs {
   int ldo;
   int nch;                         // chunks of 16 query heads per KV head slot
   int* counters;                   // [nseq*nkv*nch] CTAs that have left their part of an item, zero between calls
-  float* parts;                    // [grid][3][kDecPartFloats]: 16 x 128 output, 16 max, 16 sum
+  float* parts;                    // [grid][2][kDecPartFloats]: 16 x 128 output, 16 max, 16 sum
+  float* item_parts;               // [nseq*nkv*nch][kDecPartFloats], behind a prefix
   const float *prefix_parts, *prefix_ml;   // parts of the prefix kernel (see AttnArgs), or null
   int prefix_tiles, prefix_splits;
   unsigned long long timeout_ns;
