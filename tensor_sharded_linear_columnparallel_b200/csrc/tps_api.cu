@@ -1766,7 +1766,7 @@ int logits_sample(const void* logits, int logits_dtype, int64_t m, int64_t V, co
   a.min_p = min_p;
   a.out_idx = out_idx;
   a.out_logp = out_logp;
-  return tps::launch_sample(a, static_cast<cudaStream_t>(stream)) == 0 ? TPS_OK : TPS_ERR_CUDA;
+  return tps::launch_sample(a, num_sms_current(), static_cast<cudaStream_t>(stream)) == 0 ? TPS_OK : TPS_ERR_CUDA;
 }
 
 int vocab_parallel_sample(const void* X, int64_t m, int64_t H, const void* packed_w, int64_t V, int tp,

@@ -150,6 +150,7 @@ struct SampleArgs {
   const void* logits;              // [m][V]
   int f32;                         // fp32 logits, else bf16
   int m, V;
+  int slice;                       // tokens per CTA of a row's cluster, a multiple of 8
   const float* u;
   const float *temperature, *top_p, *min_p;   // [m] or null
   const int* top_k;                // [m] or null
@@ -226,7 +227,7 @@ int launch_kv_append(const KvAppendArgs& a, cudaStream_t st);
 int launch_prefix_attention(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a,
                             int grid, cudaStream_t st);
 int launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a, int grid, cudaStream_t st);
-int launch_sample(const SampleArgs& a, cudaStream_t st);
+int launch_sample(const SampleArgs& a, int num_sms, cudaStream_t st);   // chooses the slice
 int attention_smem_bytes(int two_tiles);
 // bf16_chain = 0: Y = P_0 + ... + P_{tp-1} (+ bias) in fp32; 1: every P_s rounded to
 // bf16, summed in shard order with a bf16 rounding after each addition, bias added

@@ -453,18 +453,19 @@ int launch_argmax_reduce(const void* part, int M, int tp, int per_shard_entries,
 
 int attention_smem_bytes(int two_tiles) { return two_tiles ? kAttn2SmemBytes : kAttnSmemBytes; }
 
-// Launches fn with its shared-memory opt-in (per device, remembered in *attr_done).
+// Launches fn in clusters, with its shared-memory opt-in of max_smem bytes (per device,
+// remembered in *attr_done).
 template <class... P, class... Args>
 static int launch_with_smem(void (*fn)(P...), unsigned long long* attr_done, int threads, int smem, int grid,
-                            cudaStream_t st, const Args&... args) {
+                            cudaStream_t st, int cluster, int max_smem, const Args&... args) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return -6;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(__atomic_load_n(attr_done, __ATOMIC_ACQUIRE) & bit)) {
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -6;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) != cudaSuccess) return -6;
     __atomic_fetch_or(attr_done, bit, __ATOMIC_ACQ_REL);
   }
-  LaunchCfg lc(grid, smem, st, 1, threads, true);
+  LaunchCfg lc(grid, smem, st, cluster, threads, true);
   if (cudaLaunchKernelEx(&lc.cfg, fn, args...) != cudaSuccess) return -6;
   return cudaGetLastError() == cudaSuccess ? 0 : -6;
 }
@@ -472,21 +473,22 @@ static int launch_with_smem(void (*fn)(P...), unsigned long long* attr_done, int
 int launch_attention(const CUtensorMap& tqkv, const AttnArgs& a, int two_tiles, int grid, cudaStream_t st) {
   static unsigned long long attr_done[2] = {0ull, 0ull};
   return two_tiles ? launch_with_smem(tps_attn2_kernel<ATTN_FULL>, &attr_done[1], kAttn2Threads, kAttn2SmemBytes, grid,
-                                      st, tqkv, tqkv, tqkv, a)
-                   : launch_with_smem(tps_attn_kernel, &attr_done[0], kAttnThreads, kAttnSmemBytes, grid, st, tqkv, a);
+                                      st, 1, kAttn2SmemBytes, tqkv, tqkv, tqkv, a)
+                   : launch_with_smem(tps_attn_kernel, &attr_done[0], kAttnThreads, kAttnSmemBytes, grid, st, 1,
+                                      kAttnSmemBytes, tqkv, a);
 }
 
 int launch_window_attention(const CUtensorMap& tqkv, const AttnArgs& a, int grid, cudaStream_t st) {
   static unsigned long long attr_done = 0ull;
-  return launch_with_smem(tps_attn2_kernel<ATTN_WINDOW>, &attr_done, kAttn2Threads, kAttn2SmemBytes, grid, st, tqkv,
-                          tqkv, tqkv, a);
+  return launch_with_smem(tps_attn2_kernel<ATTN_WINDOW>, &attr_done, kAttn2Threads, kAttn2SmemBytes, grid, st, 1,
+                          kAttn2SmemBytes, tqkv, tqkv, tqkv, a);
 }
 
 int launch_prefix_attention(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a,
                             int grid, cudaStream_t st) {
   static unsigned long long attr_done = 0ull;
-  return launch_with_smem(tps_attn2_kernel<ATTN_PREFIX>, &attr_done, kAttn2Threads, kAttn2SmemBytes, grid, st, tq, tk,
-                          tv, a);
+  return launch_with_smem(tps_attn2_kernel<ATTN_PREFIX>, &attr_done, kAttn2Threads, kAttn2SmemBytes, grid, st, 1,
+                          kAttn2SmemBytes, tq, tk, tv, a);
 }
 
 int launch_kv_append(const KvAppendArgs& a, cudaStream_t st) {
@@ -499,13 +501,22 @@ int launch_kv_append(const KvAppendArgs& a, cudaStream_t st) {
 
 int launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a, int grid, cudaStream_t st) {
   static unsigned long long attr_done = 0ull;
-  return launch_with_smem(tps_decode_kernel, &attr_done, kDecThreads, kDecSmemBytes, grid, st, tk, tv, a);
+  return launch_with_smem(tps_decode_kernel, &attr_done, kDecThreads, kDecSmemBytes, grid, st, 1, kDecSmemBytes, tk, tv, a);
 }
 
-int launch_sample(const SampleArgs& a, cudaStream_t st) {
-  LaunchCfg lc(a.m < 4 * 148 ? a.m : 4 * 148, 0, st, 1, kSampleThreads, true);
-  if (cudaLaunchKernelEx(&lc.cfg, tps_sample_plain_kernel, a) != cudaSuccess) return -6;
-  return cudaGetLastError() == cudaSuccess ? 0 : -6;
+// CTAs per row: as few as hold the row at 64 KB each (three CTAs fit an SM), and more, down
+// to 4096 tokens each, while the SMs are not covered: latency then goes by the passes over
+// a CTA's part.
+int launch_sample(const SampleArgs& a, int num_sms, cudaStream_t st) {
+  int cs = 1;
+  while (cs < 8 && a.V > cs * 16384) cs *= 2;
+  while (cs < 8 && static_cast<long long>(a.m) * cs < num_sms && a.V > cs * 4096) cs *= 2;
+  if (static_cast<long long>(a.m) * cs > 0x7fffffffLL) return -6;
+  SampleArgs b = a;
+  b.slice = ((a.V + cs - 1) / cs + 7) / 8 * 8;
+  static unsigned long long attr_done = 0ull;
+  return launch_with_smem(tps_sample_kernel, &attr_done, kSampleThreads, sample_smem_bytes(b.slice), a.m * cs, st, cs,
+                          sample_smem_bytes(static_cast<int>(kSampleMaxVocab / 8)), b);
 }
 
 int launch_gemm(int swap, int bn, int dual, const CUtensorMap& tx, const CUtensorMap& tw, const GemmArgs& a,
