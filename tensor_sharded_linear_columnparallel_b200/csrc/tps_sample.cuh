@@ -10,10 +10,12 @@
 // Every filter keeps a top part of the order (logit descending, index ascending), so a
 // row's filters are one threshold, the last kept token, and no sort of the row is needed.
 // One thread-block cluster holds a row in the shared memory of its CTAs (fp32, read once
-// from HBM) and finds the threshold from a histogram of 1024 equal bins over the logits
-// within 32 T of the maximum (what lies below has no weight): counts for top-k, exact
-// weights for top-p, so the bin that holds the cut is known. The tokens of that bin go to
-// the first CTA. When the k largest fit its list of 1024 it takes both cuts there, and with
+// from HBM) and finds the threshold from a histogram of up to 1024 equal bins over the
+// logits within 32 T of the maximum (what lies below has no weight): counts, and for top-p
+// weights as 16-bit numbers (a shift per octave of bins, so that a bin's sum keeps its
+// relative precision and fits 32 bits), whose truncation leaves one or two bins that can
+// hold the cut. The tokens of those bins go to the first CTA, which takes the cut from exact
+// sums. When the k largest fit its list of 1024 it takes both cuts there, and with
 // up to 256 of them it draws there too: each token finds its own place by comparing itself
 // with the others, which needs no sort and no further step of the cluster. Where the bin
 // holds more than the list (equal logits, one far outlier that stretches the bins), the
@@ -29,10 +31,9 @@ namespace tps {
 
 typedef unsigned long long u64;
 
-constexpr int kSampleThreads = 512;
-constexpr int kSampleWarps = kSampleThreads / 32;
+constexpr int kSampleMaxWarps = 32;
 constexpr int kSampleBins = 1024;
-constexpr int kSampleList = 1024;              // entries of the candidate list, which overlays the histogram's weights
+constexpr int kSampleList = 1024;              // entries of the candidate list, which overlays the histogram
 constexpr u64 kSampleOne = 1ull << 44;         // weight of the largest logit
 constexpr int kSampleSmall = 256;              // kept tokens that the first CTA draws from by itself
 
@@ -41,9 +42,9 @@ __device__ __forceinline__ uint32_t atomic_add_cluster_u32(uint32_t addr, uint32
   asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(v) : "r"(addr), "r"(x) : "memory");
   return v;
 }
-__device__ __forceinline__ u64 ld_cluster_u64(uint32_t addr) {
-  u64 v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, u64 v) {
@@ -64,47 +65,45 @@ __device__ __forceinline__ u64 sample_rank(float x, int i) {
 // A NaN logit is never drawn; -0 equals +0.
 __device__ __forceinline__ float sample_clean(float x) { return x == x ? x + 0.0f : -INFINITY; }
 
-// 2^-y for y >= 0 in units of 2^-44, rounded: y = n + f with f in [-1/2, 1/2], 2^-f as its
-// Taylor sum to (f ln 2)^11 / 11! (the rest is below 2^-47), the power of two put into the
-// exponent field, and the integer read from the low bits after adding 2^52.
-__device__ __forceinline__ u64 sample_exp2(double y) {
-  if (!(y < 46.0)) return 0ull;
-  const double t = y + 6755399441055744.0;                  // 1.5 * 2^52: y rounded to an integer, in the low bits
-  const int n = static_cast<int>(__double2loint(t));
-  const double f = (t - 6755399441055744.0) - y;
-  double p = 4.4455382718708115e-10;                        // ln(2)^k / k!, k = 11 ... 0
-  p = fma(p, f, 7.0549116208011233e-09);
-  p = fma(p, f, 1.0178086009239699e-07);
-  p = fma(p, f, 1.3215486790144310e-06);
-  p = fma(p, f, 1.5252733804059840e-05);
-  p = fma(p, f, 1.5403530393381609e-04);
-  p = fma(p, f, 1.3333558146428443e-03);
-  p = fma(p, f, 9.6181291076284772e-03);
-  p = fma(p, f, 5.5504108664821580e-02);
-  p = fma(p, f, 2.4022650695910072e-01);
-  p = fma(p, f, 6.9314718055994531e-01);
-  p = fma(p, f, 1.0);
-  const double v = __hiloint2double(__double2hiint(p) + ((44 - n) << 20), __double2loint(p));   // p * 2^(44 - n)
-  return static_cast<u64>(__double_as_longlong(v + 4503599627370496.0)) & ((1ull << 52) - 1);
-}
-
 struct SampleRow {             // one row's parameters, the same in every CTA of its cluster
-  float mx;                    // largest logit
-  double c;                    // log2(e) / T
-  float bin_scale;             // bins per logit
-  double q;                    // min_p in units of 2^-44
+  double mx, c;                // largest logit; log2(e) / T
+  float mxf;                   // largest logit
+  float bin_scale;             // bins per logit: 2^octave of them per factor of 2 in the weight
+  int octave;                  // (31 for more: all bins are within one factor)
+  u64 q;                       // min_p in units of 2^-44
 };
 
+// exp((x - mx) / T) in units of 2^-44, without a branch: 2^-y with y = (mx - x) log2(e) / T =
+// n + f, f in [-1/2, 1/2], 2^-f as its Taylor sum to (f ln 2)^9 / 9! (the rest is below
+// 2^-37), the power of two put into the exponent field, and the integer read from the low
+// bits after adding 2^52. The largest logit gives exactly 2^44; a y above 46 counts as 46,
+// whose weight rounds to 0.
 __device__ __forceinline__ u64 sample_weight(float x, const SampleRow& r) {
-  if (!(x > -INFINITY)) return 0ull;
-  if (x == r.mx) return kSampleOne;
-  return sample_exp2((static_cast<double>(r.mx) - static_cast<double>(x)) * r.c);   // mx = inf: 0
+  const double y = fmin((r.mx - static_cast<double>(x)) * r.c, 46.0);
+  const double t = y + 6755399441055744.0;                  // 1.5 * 2^52: y rounded to an integer, in the low bits
+  const double f = (t - 6755399441055744.0) - y;
+  double p = 1.0178086009239700e-07;                        // ln(2)^k / k!, k = 9 ... 0
+  p = fma(p, f, 1.3215486790144310e-06);
+  p = fma(p, f, 1.5252733804059841e-05);
+  p = fma(p, f, 1.5403530393381610e-04);
+  p = fma(p, f, 1.3333558146428443e-03);
+  p = fma(p, f, 9.6181291076284770e-03);
+  p = fma(p, f, 5.5504108664821580e-02);
+  p = fma(p, f, 2.4022650695910072e-01);
+  p = fma(p, f, 6.9314718055994530e-01);
+  p = fma(p, f, 1.0);
+  const double v = __hiloint2double(__double2hiint(p) + ((44 - __double2loint(t)) << 20), __double2loint(p));
+  const double m = v + 4503599627370496.0;                  // 2^52
+  return static_cast<u64>(static_cast<uint32_t>(__double2hiint(m)) & 0xfffffu) << 32 |
+         static_cast<uint32_t>(__double2loint(m));
 }
 
-// Bin of a logit: 0 holds the largest, the last one everything from 32 T below it on.
+// Bin of a logit: 0 holds the largest, the last one everything beyond.
 __device__ __forceinline__ int sample_bin(float x, const SampleRow& r) {
-  return x == r.mx ? 0 : static_cast<int>(fminf((r.mx - x) * r.bin_scale, static_cast<float>(kSampleBins - 1)));
+  return static_cast<int>(fminf((r.mxf - x) * r.bin_scale, static_cast<float>(kSampleBins - 1)));
 }
+// Weights of bin b are below 2^(16 + shift): the bin spans less than one octave of weights.
+__device__ __forceinline__ int sample_shift(int b, const SampleRow& r) { return max(0, 29 - (b >> r.octave)); }
 
 // What the first CTA tells the others about the next step (one copy per CTA).
 struct SampleCmd {
@@ -116,17 +115,17 @@ struct SampleCmd {
 };
 
 struct SampleSmem {
-  u64 red[kSampleWarps];
+  u64 red[kSampleMaxWarps];
   u64 part[2][8];              // values that the CTAs of the cluster exchange, two in turn
   u64 top[8];
   SampleCmd cmd;
   int listed;                  // first CTA: list entries handed out to the CTAs
   int place;                   // next free entry of this CTA's
-  float fred[2 * kSampleWarps];
+  float fred[2 * kSampleMaxWarps];
 };
 
 constexpr int kSampleHead = (static_cast<int>(sizeof(SampleSmem)) + 15) / 16 * 16;
-constexpr int sample_smem_bytes(int slice) { return kSampleHead + kSampleBins * 12 + slice * 4; }
+constexpr int sample_smem_bytes(int slice) { return kSampleHead + kSampleBins * 8 + slice * 4; }
 
 template <class T, class Op>
 __device__ __forceinline__ T sample_warp_reduce(T v, Op op) {
@@ -134,46 +133,49 @@ __device__ __forceinline__ T sample_warp_reduce(T v, Op op) {
   for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
+// Sum over the block, in every thread.
+template <int THREADS>
 __device__ __forceinline__ u64 sample_block_sum(u64 v, SampleSmem& s) {
   v = sample_warp_reduce(v, [](u64 x, u64 y) { return x + y; });
   __syncthreads();
   if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = 0;
-#pragma unroll
-  for (int i = 0; i < kSampleWarps; ++i) v += s.red[i];
-  return v;
+  v = (threadIdx.x & 31) < THREADS / 32 ? s.red[threadIdx.x & 31] : 0;
+  return sample_warp_reduce(v, [](u64 x, u64 y) { return x + y; });
 }
 // Exclusive sum over the block, and the total.
+template <int THREADS>
 __device__ __forceinline__ u64 sample_block_scan(u64 v, u64& total, SampleSmem& s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  u64 incl = v;
+  auto scan = [&](u64 x) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const u64 n = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += n;
-  }
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 n = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += n;
+    }
+    return x;
+  };
+  const u64 incl = scan(v);
   __syncthreads();
   if (lane == 31) s.red[warp] = incl;
   __syncthreads();
-  u64 before = 0;
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < kSampleWarps; ++i) {
-    if (i < warp) before += s.red[i];
-    total += s.red[i];
-  }
-  return before + incl - v;
+  const u64 w = lane < THREADS / 32 ? s.red[lane] : 0;
+  const u64 ws = scan(w);
+  total = __shfl_sync(0xffffffffu, ws, 31);
+  return __shfl_sync(0xffffffffu, ws - w, warp) + incl - v;
 }
 
-__global__ void __launch_bounds__(kSampleThreads) tps_sample_kernel(const SampleArgs a) {
+template <int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleArgs a) {
+  constexpr int WARPS = THREADS / 32;
+  constexpr int BPT = kSampleBins / THREADS;     // bins (and list entries) per thread
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SampleSmem& s = *reinterpret_cast<SampleSmem*>(smem_raw);
-  u64* mass = reinterpret_cast<u64*>(smem_raw + kSampleHead);
-  u64* list = mass;
-  uint32_t* cnt = reinterpret_cast<uint32_t*>(mass + kSampleBins);
-  float* xs = reinterpret_cast<float*>(cnt + kSampleBins);
-  static_assert(kSampleList <= kSampleBins && kSampleBins == 2 * kSampleThreads, "shared memory layout");
+  uint32_t* cnt = reinterpret_cast<uint32_t*>(smem_raw + kSampleHead);
+  uint32_t* mass = cnt + kSampleBins;
+  u64* list = reinterpret_cast<u64*>(cnt);
+  float* xs = reinterpret_cast<float*>(mass + kSampleBins);
+  static_assert(kSampleList <= kSampleBins && 2 * kSampleSmall <= THREADS, "shared memory layout");
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cs = static_cast<int>(cluster_nctarank()), cr = static_cast<int>(cluster_ctarank());
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kSampleThreads) tps_sample_kernel(const Sample
     const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) +
                                                         static_cast<long long>(row) * a.V + i0);
 #pragma unroll 8
-    for (int v = tid; v < n / 4; v += kSampleThreads) {
+    for (int v = tid; v < n / 4; v += THREADS) {
       float4 x = __ldcs(src + v);
       x = make_float4(sample_clean(x.x), sample_clean(x.y), sample_clean(x.z), sample_clean(x.w));
       reinterpret_cast<float4*>(xs)[v] = x;
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(kSampleThreads) tps_sample_kernel(const Sample
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.logits) +
                                                       static_cast<long long>(row) * a.V + i0);
 #pragma unroll 4
-    for (int v = tid; v < n / 8; v += kSampleThreads) {
+    for (int v = tid; v < n / 8; v += THREADS) {
       const uint4 b = __ldcs(src + v);
       const uint32_t w[4] = {b.x, b.y, b.z, b.w};
       float x[8];
@@ -228,16 +230,16 @@ __global__ void __launch_bounds__(kSampleThreads) tps_sample_kernel(const Sample
       for (int j = 0; j < 8; ++j) take(x[j]);
     }
   }
-  for (int j = tid; j < kSampleBins; j += kSampleThreads) cnt[j] = 0, mass[j] = 0;
+  for (int j = tid; j < kSampleBins; j += THREADS) cnt[j] = mass[j] = 0;
   if (tid == 0) s.listed = s.cmd.drawn = 0;
   mx = sample_warp_reduce(mx, [](float x, float y) { return fmaxf(x, y); });
   mn = sample_warp_reduce(mn, [](float x, float y) { return fminf(x, y); });
-  if (lane == 0) s.fred[warp] = mx, s.fred[kSampleWarps + warp] = mn;
+  if (lane == 0) s.fred[warp] = mx, s.fred[WARPS + warp] = mn;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kSampleWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     mx = fmaxf(mx, s.fred[w]);
-    mn = fminf(mn, s.fred[kSampleWarps + w]);
+    mn = fminf(mn, s.fred[WARPS + w]);
   }
   if (tid < cs)
     st_cluster_u64(remote(&s.top[cr], tid), static_cast<u64>(__float_as_uint(mx)) << 32 | __float_as_uint(mn));
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(kSampleThreads) tps_sample_kernel(const Sample
   float cx = -INFINITY;                        // kept: x > cx, or x == cx and index <= ci (and min_p)
   int ci = -1;
   auto each = [&](auto f) {                    // every kept token of this CTA (never a logit of -inf)
-    for (int v = tid; v < n / 4; v += kSampleThreads) {
+    for (int v = tid; v < n / 4; v += THREADS) {
       const float4 q = reinterpret_cast<const float4*>(xs)[v];
       const float x[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(kSampleThreads) tps_sample_kernel(const Sample
     __syncthreads();
     if (lane == 0) s.red[warp] = static_cast<u64>(arg);
     __syncthreads();
-    for (int w = 0; w < kSampleWarps; ++w) arg = min(arg, static_cast<int>(s.red[w]));
+    for (int w = 0; w < WARPS; ++w) arg = min(arg, static_cast<int>(s.red[w]));
     if (tid == 0) st_cluster_u64(remote(&s.part[0][cr], 0), static_cast<u64>(arg));
     cluster_sync_all();
     if (cr == 0 && tid == 0) {
@@ -283,14 +285,25 @@ __global__ void __launch_bounds__(kSampleThreads) tps_sample_kernel(const Sample
     }
     return;
   }
+  if (mx == INFINITY) {                        // +inf logits share the weight: as 0 among -inf
+    for (int j = tid; j < n; j += THREADS) xs[j] = xs[j] == INFINITY ? 0.0f : -INFINITY;
+    mx = mn = 0.0f;
+    __syncthreads();
+  }
   SampleRow r;
-  r.mx = mx;
+  r.mxf = mx;
+  r.mx = static_cast<double>(mx);
   r.c = 1.4426950408889634 / static_cast<double>(T);
-  r.q = a.min_p ? static_cast<double>(a.min_p[row]) * static_cast<double>(kSampleOne) : 0.0;
-  const float range = fminf(mx - mn, 32.0f * T);
-  r.bin_scale = range > 0.0f ? static_cast<float>(kSampleBins - 1) / range : 0.0f;
+  r.q = 0;
+  if (a.min_p && a.min_p[row] > 0.0f)
+    r.q = static_cast<u64>(ceil(fmin(static_cast<double>(a.min_p[row]), 1.0) * static_cast<double>(kSampleOne)));
+  // 2^octave bins per factor of 2: as many as keep the range within the bins
+  const double span = fmin((r.mx - static_cast<double>(mn)) * r.c, 46.2);   // in factors of 2; 46.2 = 32 log2(e)
+  const int octave = span > 0.0 ? min(100, ilogb(static_cast<double>(kSampleBins - 1) / span)) : 0;   // at least 4
+  r.bin_scale = static_cast<float>(fmin(scalbn(r.c, octave), 3e38));
+  r.octave = min(octave, 31);
   const double p = static_cast<double>(pf);
-  auto survives = [&](u64 w) { return w == kSampleOne || static_cast<double>(w) >= r.q; };   // min_p
+  auto survives = [&](u64 w) { return w >= r.q; };         // min_p
   auto goal = [&](u64 total) {                 // the draw falls on the token whose running sum exceeds this
     const u64 t = static_cast<u64>(u * static_cast<double>(total));
     return t < total ? t : total - 1;
@@ -309,7 +322,7 @@ __global__ void __launch_bounds__(kSampleThreads) tps_sample_kernel(const Sample
       each([&](float x, int i) {
         if (sample_rank(x, i) >= c) v += by_weight ? sample_weight(x, r) : 1ull;
       });
-      v = cluster_all(sample_block_sum(v, s));
+      v = cluster_all(sample_block_sum<THREADS>(v, s));
       if (by_weight ? (v > 0 && static_cast<double>(v) >= target) : v >= want) t = c;
     }
     return t;
@@ -326,50 +339,78 @@ __global__ void __launch_bounds__(kSampleThreads) tps_sample_kernel(const Sample
   enum { NOTHING, DRAW, CUT_P };
   auto cut = [&](int k, bool by_p) -> int {
     u64 sum = 0;
-    each([&](float x, int) {
-      const int b = sample_bin(x, r);
-      atomicAdd(cnt + b, 1u);
-      if (k == 0) {
+    if (k > 0) {
+      each([&](float x, int) { atomicAdd(cnt + sample_bin(x, r), 1u); });
+      __syncthreads();
+    } else {
+      each([&](float x, int) {
+        const int b = sample_bin(x, r);
         const u64 w = sample_weight(x, r);
         sum += w;
-        if (w) atomicAdd(mass + b, w);
-      }
-    });
-    if (k == 0) sum = sample_block_sum(sum, s);
-    else __syncthreads();
+        atomicAdd(cnt + b, 1u);
+        atomicAdd(mass + b, static_cast<uint32_t>(w >> sample_shift(b, r)));
+      });
+      sum = sample_block_sum<THREADS>(sum, s);
+    }
     const u64 total = cluster_all(sum);
     if (cr == 0) {
-      // bins 2 tid and 2 tid + 1 over the cluster: what lies before each, in tokens or weight
-      u64 c2[2] = {0, 0}, v2[2] = {0, 0}, all;
-#pragma unroll 4
-      for (int q = 0; q < cs; ++q) {
-        const u64 c = ld_cluster_u64(remote(cnt + 2 * tid, q));
-        c2[0] += c & 0xffffffffu, c2[1] += c >> 32;
-        if (k == 0) {
-          v2[0] += ld_cluster_u64(remote(mass + 2 * tid, q));
-          v2[1] += ld_cluster_u64(remote(mass + 2 * tid + 1, q));
-        }
+      // BPT bins per thread over the cluster: what lies before each, in tokens or in weight (a
+      // lower and an upper bound)
+      u64 c[BPT], lo[BPT], hi[BPT], lsum = 0, hsum = 0, all, unused;
+#pragma unroll
+      for (int j = 0; j < BPT; ++j) {
+        const int b = tid * BPT + j;
+        u64 m = 0;
+        c[j] = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < cs) {
+            c[j] += ld_cluster_u32(remote(cnt + b, q));
+            if (k == 0) m += ld_cluster_u32(remote(mass + b, q));
+          }
+        lo[j] = k > 0 ? c[j] : m << sample_shift(b, r);
+        hi[j] = k > 0 ? c[j] : (m + c[j]) << sample_shift(b, r);
+        lsum += lo[j];
+        hsum += hi[j];
       }
-      if (k > 0) v2[0] = c2[0], v2[1] = c2[1];
-      const u64 before = sample_block_scan(v2[0] + v2[1], all, s);
-      const u64 cum[3] = {before, before + v2[0], before + v2[0] + v2[1]};
-      if (tid == 0) s.cmd.n = -2;              // k >= the number of tokens
+      u64 lb = sample_block_scan<THREADS>(lsum, all, s);
+      u64 hb = k > 0 ? lb : sample_block_scan<THREADS>(hsum, unused, s);
+      if (tid == 0) {
+        s.cmd.lo = 0;                          // set below by the bins that the cut can lie in
+        s.cmd.hi = kSampleBins - 1;
+        s.cmd.n = k > 0 && static_cast<u64>(k) >= all ? -2 : 0;
+        s.cmd.total = total;
+      }
       __syncthreads();
       const double target = k > 0 ? static_cast<double>(k) : p * static_cast<double>(total);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        // the bin in which the running value reaches the target (the first that has any for a target of 0)
-        const bool reaches = v2[j] > 0 && static_cast<double>(cum[j + 1]) >= target &&
-                             (cum[j] == 0 || static_cast<double>(cum[j]) < target);
-        if (reaches && (k == 0 || static_cast<u64>(k) < all)) {
-          const bool from0 = k > 0 && cum[j + 1] <= kSampleList;   // every kept token fits the list
-          s.cmd.lo = from0 ? 0 : 2 * tid + j;
-          s.cmd.hi = 2 * tid + j;
-          const u64 len = from0 ? cum[j + 1] : c2[j];
-          s.cmd.n = len > kSampleList ? -1 : static_cast<int>(len);
-          s.cmd.total = k == 0 ? total : from0 ? 0 : cum[j];
-          s.cmd.C = k == 0 ? cum[j] : 0;       // weight above the list
+      for (int j = 0; j < BPT; ++j) {          // the first bin that may reach the target, and the first that must
+        if (static_cast<double>(hb) < target && static_cast<double>(hb + hi[j]) >= target) s.cmd.lo = tid * BPT + j;
+        if (static_cast<double>(lb) < target && static_cast<double>(lb + lo[j]) >= target) {
+          s.cmd.hi = tid * BPT + j;
+          if (k > 0) s.cmd.total = lb;
         }
+        hb += hi[j];
+        lb += lo[j];
+      }
+      if (!(target > 0.0) && tid == 0) s.cmd.hi = 0;       // the largest logit alone: bin 0 has it
+      __syncthreads();
+      u64 listed = 0, before = 0;
+#pragma unroll
+      for (int j = 0; j < BPT; ++j) {
+        const int b = tid * BPT + j;
+        if (b >= s.cmd.lo && b <= s.cmd.hi) listed += c[j];
+        if (b < s.cmd.lo) before += c[j];
+      }
+      listed = sample_block_sum<THREADS>(listed, s);
+      before = sample_block_sum<THREADS>(before, s);
+      if (tid == 0 && s.cmd.n == 0) {
+        if (k > 0 && before + listed <= kSampleList) {     // every kept token fits the list
+          s.cmd.lo = 0;
+          s.cmd.total = 0;
+          listed += before;
+        }
+        s.cmd.n = listed > kSampleList ? -1 : static_cast<int>(listed);
       }
       __syncthreads();
       // the command to the other CTAs
@@ -377,65 +418,71 @@ __global__ void __launch_bounds__(kSampleThreads) tps_sample_kernel(const Sample
         for (int q = 1; q < cs; ++q)
           st_cluster_u64(remote(reinterpret_cast<u64*>(&s.cmd) + tid, q), reinterpret_cast<const u64*>(&s.cmd)[tid]);
     }
-    cluster_sync_all();                        // also: the histograms' weights have been read, the list may overwrite them
+    cluster_sync_all();                        // also: the first CTA has read the histograms
     const SampleCmd cmd = s.cmd;
     const int after = by_p && k > 0 ? CUT_P : DRAW;
     if (cmd.n < 0) {
       if (cmd.n == -1)
         set_threshold(k > 0 ? bisect(false, static_cast<u64>(k), 0.0)
                             : bisect(true, 0, p * static_cast<double>(cmd.total)));
-      for (int j = tid; j < kSampleBins; j += kSampleThreads) cnt[j] = 0, mass[j] = 0;
+      for (int j = tid; j < kSampleBins; j += THREADS) cnt[j] = 0, mass[j] = 0;
       __syncthreads();
       return after;
     }
     // this CTA's place in the list: as many entries as its own histogram says
     u64 c = 0;
-    for (int b = cmd.lo + tid; b <= cmd.hi; b += kSampleThreads) c += cnt[b];
-    c = sample_block_sum(c, s);
-    if (tid == 0) s.place = c ? static_cast<int>(atomic_add_cluster_u32(remote(&s.listed, 0), static_cast<uint32_t>(c))) : 0;
-    __syncthreads();
-    if (c)
+    for (int b = cmd.lo + tid; b <= cmd.hi; b += THREADS) c += cnt[b];
+    c = sample_block_sum<THREADS>(c, s);
+    if (tid == 0)
+      s.place = c ? static_cast<int>(atomic_add_cluster_u32(remote(&s.listed, 0), static_cast<uint32_t>(c))) : 0;
+    cluster_sync_all();                        // every CTA has read its histogram: the list may overwrite the first one's
+    u64 above = 0;                             // weight above the list
+    if (c || k == 0)
       each([&](float x, int i) {
         const int b = sample_bin(x, r);
         if (b >= cmd.lo && b <= cmd.hi) st_cluster_u64(remote(list + atomicAdd(&s.place, 1), 0), sample_rank(x, i));
+        else if (k == 0 && b < cmd.lo) above += sample_weight(x, r);
       });
-    for (int j = tid; j < kSampleBins; j += kSampleThreads) {   // for a second cut
-      cnt[j] = 0;
-      if (cr > 0) mass[j] = 0;
-    }
-    cluster_sync_all();
+    if (cr > 0)                                // for a second cut
+      for (int j = tid; j < kSampleBins; j += THREADS) cnt[j] = mass[j] = 0;
+    above = cluster_all(k == 0 ? sample_block_sum<THREADS>(above, s) : 0);
     const bool whole = k > 0 && cmd.lo == 0;   // the list begins at the top
     if (cr == 0) {
       const int len = cmd.n;
       if (whole && len <= kSampleSmall) {
-        // Two threads per token e: how many tokens come before it and their weight, then the
+        // THREADS / 256 threads per token e: how many tokens come before it and their weight, then the
         // weight of the kept tokens up to it in vocabulary order.
-        const int e = tid >> 1, half = tid & 1;
+        constexpr int TPE = THREADS / kSampleSmall;
+        const int e = tid / TPE, half = tid % TPE;
         const u64 re = e < len ? list[e] : 0;
         const u64 we = e < len ? sample_weight(sample_unkey(static_cast<uint32_t>(re >> 32)), r) : 0;
         u64* w = list + kSampleSmall;          // weights, by list entry (each pair writes its own)
         if (half == 0) w[e] = we;
         __syncthreads();
         int place = 0;
-        u64 above = 0;
-        for (int j = half; j < len; j += 2)
-          if (list[j] > re) ++place, above += w[j];
-        place += __shfl_xor_sync(0xffffffffu, place, 1);
-        above += __shfl_xor_sync(0xffffffffu, above, 1);
+        u64 larger = 0;
+        for (int j = half; j < len; j += TPE)
+          if (list[j] > re) ++place, larger += w[j];
+#pragma unroll
+        for (int o = 1; o < TPE; o <<= 1) {
+          place += __shfl_xor_sync(0xffffffffu, place, o);
+          larger += __shfl_xor_sync(0xffffffffu, larger, o);
+        }
         bool in = e < len && place < k;
         if (by_p) {
-          const u64 wk = sample_block_sum(in && half == 0 ? we : 0, s);
-          in = in && (place == 0 || static_cast<double>(above) < p * static_cast<double>(wk));
+          const u64 wk = sample_block_sum<THREADS>(in && half == 0 ? we : 0, s);
+          in = in && (place == 0 || static_cast<double>(larger) < p * static_cast<double>(wk));
         }
         in = in && survives(we);
         __syncthreads();
         if (half == 0) w[e] = in ? we : 0;
-        const u64 tot = sample_block_sum(in && half == 0 ? we : 0, s);
+        const u64 tot = sample_block_sum<THREADS>(in && half == 0 ? we : 0, s);
         const uint32_t ie = static_cast<uint32_t>(re);           // ~index: larger is earlier
         u64 upto = 0;
-        for (int j = half; j < len; j += 2)
+        for (int j = half; j < len; j += TPE)
           if (static_cast<uint32_t>(list[j]) >= ie) upto += w[j];
-        upto += __shfl_xor_sync(0xffffffffu, upto, 1);
+#pragma unroll
+        for (int o = 1; o < TPE; o <<= 1) upto += __shfl_xor_sync(0xffffffffu, upto, o);
         const u64 t = goal(tot);
         if (in && half == 0 && upto > t && upto - we <= t) draw(static_cast<int>(0xffffffffu - ie), we, tot);
         if (tid < cs) {
@@ -446,11 +493,11 @@ __global__ void __launch_bounds__(kSampleThreads) tps_sample_kernel(const Sample
       } else {
         int m = 32;                            // bitonic sort, descending, padded with zeros
         while (m < len) m <<= 1;
-        for (int j = len + tid; j < m; j += kSampleThreads) list[j] = 0;
+        for (int j = len + tid; j < m; j += THREADS) list[j] = 0;
         __syncthreads();
         for (int size = 2; size <= m; size <<= 1)
           for (int d = size >> 1; d > 0; d >>= 1) {
-            for (int j = tid; j < m / 2; j += kSampleThreads) {
+            for (int j = tid; j < m / 2; j += THREADS) {
               const int lo = 2 * j - (j & (d - 1)), hi = lo + d;
               const u64 x = list[lo], y = list[hi];
               if ((x < y) == ((lo & size) == 0)) list[lo] = y, list[hi] = x;
@@ -460,22 +507,27 @@ __global__ void __launch_bounds__(kSampleThreads) tps_sample_kernel(const Sample
         const int kk = k > 0 ? k - static_cast<int>(cmd.total) : len;   // entries that may stay
         int last = kk - 1;                     // the last kept one
         if (k == 0 || (whole && by_p)) {
-          u64 w[2], tot;                       // entries 2 tid and 2 tid + 1: the weight before each
+          u64 w[BPT], sum = 0, tot;            // BPT entries per thread: the weight before each
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            w[j] = 2 * tid + j < kk ? sample_weight(sample_unkey(static_cast<uint32_t>(list[2 * tid + j] >> 32)), r) : 0;
-          const u64 before = sample_block_scan(w[0] + w[1], tot, s) + (k == 0 ? cmd.C : 0);
+          for (int j = 0; j < BPT; ++j) {
+            w[j] = tid * BPT + j < kk
+                       ? sample_weight(sample_unkey(static_cast<uint32_t>(list[tid * BPT + j] >> 32)), r) : 0;
+            sum += w[j];
+          }
+          u64 before = sample_block_scan<THREADS>(sum, tot, s) + above;
           const double target = p * static_cast<double>(k == 0 ? cmd.total : tot);
           u64 kept = 0;
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            kept += 2 * tid + j < kk && static_cast<double>(before + (j ? w[0] : 0)) < target;
-          last = max(static_cast<int>(sample_block_sum(kept, s)), 1) - 1;
+          for (int j = 0; j < BPT; ++j) {
+            kept += tid * BPT + j < kk && static_cast<double>(before) < target;
+            before += w[j];
+          }
+          last = max(static_cast<int>(sample_block_sum<THREADS>(kept, s)), 1) - 1;
         }
         const u64 C = list[last];
         __syncthreads();
         if (tid < cs) st_cluster_u64(remote(&s.cmd.C, tid), C);
-        for (int j = tid; j < kSampleBins; j += kSampleThreads) mass[j] = 0;
+        for (int j = tid; j < kSampleBins; j += THREADS) cnt[j] = mass[j] = 0;
         if (tid == 0) s.listed = 0;
       }
     }
@@ -491,24 +543,26 @@ __global__ void __launch_bounds__(kSampleThreads) tps_sample_kernel(const Sample
   if (left == NOTHING) return;
 
   // ------------------------------------------------ the draw, in vocabulary order: a warp has a contiguous part
-  const int per = (((n + kSampleWarps - 1) / kSampleWarps) + 31) & ~31;
+  const int per = (((n + WARPS - 1) / WARPS) + 127) & ~127;
   const int j0 = min(n, warp * per), j1 = min(n, j0 + per);
-  auto kept = [&](int j) -> u64 {
-    const float x = j < j1 ? xs[j] : -INFINITY;
-    if (!(x > cx || (x == cx && i0 + j <= ci))) return 0ull;
+  auto kept = [&](float x, int j) -> u64 {
     const u64 w = sample_weight(x, r);
-    return survives(w) ? w : 0ull;
+    const bool in = x > cx || (x == cx && i0 + j <= ci);
+    return in && survives(w) ? w : 0ull;
   };
   u64 mine = 0;
-#pragma unroll 4
-  for (int j = j0 + lane; j < j1; j += 32) mine += kept(j);
+  for (int j = j0 + 4 * lane; j < j1; j += 128) {
+    const float4 x = *reinterpret_cast<const float4*>(xs + j);
+    if (fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) >= cx)     // few lanes have any behind a filter
+      mine += (kept(x.x, j) + kept(x.y, j + 1)) + (kept(x.z, j + 2) + kept(x.w, j + 3));
+  }
   mine = sample_warp_reduce(mine, [](u64 x, u64 y) { return x + y; });
   __syncthreads();
   if (lane == 0) s.red[warp] = mine;
   __syncthreads();
   u64 before = 0, block = 0;
 #pragma unroll
-  for (int w = 0; w < kSampleWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += s.red[w];
     block += s.red[w];
   }
@@ -522,7 +576,7 @@ __global__ void __launch_bounds__(kSampleThreads) tps_sample_kernel(const Sample
   const u64 target = goal(total);
   if (before <= target && target < before + mine) {
     for (int jb = j0; jb < j1; jb += 32) {
-      const u64 w = kept(jb + lane);
+      const u64 w = jb + lane < j1 ? kept(xs[jb + lane], jb + lane) : 0;
       u64 incl = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
