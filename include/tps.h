@@ -421,11 +421,12 @@ TPS_API size_t tps_decode_workspace_bytes(int64_t nseq, const tps_heads* heads, 
  *     out_logp = log of the drawn token's share of the kept weight
  *   u, temperature, top_p, min_p: device fp32 [m]; top_k: device int32 [m]; u in [0, 1)
  *   (values outside are taken as its ends). temperature, top_k, top_p, min_p may be NULL:
- *   1, all, all, all. temperature <= 0 (or NaN) is greedy: the largest logit, the lowest
- *   index on ties. Logits of -inf and NaN are never drawn; +inf logits share the weight
+ *   1, all, all, all. temperature < 2^-100 (or NaN) is greedy: the largest logit, the
+ *   lowest index on ties. Logits of -inf and NaN are never drawn; +inf logits share the weight
  *   equally; a row without any other logit gives out_idx -1 and out_logp -inf.
- *   Weights and sums are 64-bit integers in units of 2^-44 of the largest weight, so a
- *   result depends neither on the order of the additions nor on the launch.
+ *   Weights are 64-bit integers in units of 2^-44 of the largest one, within 2^-36 of
+ *   their value (relative) and half a unit; sums of them are exact, so a result depends
+ *   neither on the order of the additions nor on the launch.
  *   out_logp: device fp32 [m] or NULL. V must be a multiple of 8 (TPS_ERR_ALIGN) and at
  *   most 393216 (TPS_ERR_UNIMPLEMENTED). Errors: TPS_ERR_ARG, TPS_ERR_DTYPE,
  *   TPS_ERR_ALIGN, TPS_ERR_DEVICE, TPS_ERR_CUDA.

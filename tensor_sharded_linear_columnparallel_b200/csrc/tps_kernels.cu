@@ -504,9 +504,20 @@ int launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs
   return launch_with_smem(tps_decode_kernel, &attr_done, kDecThreads, kDecSmemBytes, grid, st, 1, kDecSmemBytes, tk, tv, a);
 }
 
-// CTAs per row: as few as hold the row at 64 KB each (two CTAs of 512 threads fit an SM),
-// and more, down to 4096 tokens each, while the SMs are not covered: latency then goes by
-// the passes over a CTA's part, which 1024 threads shorten.
+// CTAs per row: as few as hold it at 16384 tokens each, and more, down to 4096 tokens each,
+// while the SMs are not covered. Few rows go by latency: 1024 threads shorten the passes over
+// a CTA's part. Many go by throughput: of CTAs with 256 threads four fit an SM (three with
+// fp32 logits), so a batch of 64 rows of a 128256-token vocabulary runs in one wave.
+template <class E>
+static int launch_sample_type(const SampleArgs& a, int cs, int num_sms, cudaStream_t st) {
+  const int smem = sample_smem_bytes(a.slice, a.f32);
+  const int max_smem = sample_smem_bytes(static_cast<int>(kSampleMaxVocab / 8), a.f32);
+  static unsigned long long attr_done[2] = {0ull, 0ull};
+  if (static_cast<long long>(a.m) * cs <= num_sms && a.slice > 2048)
+    return launch_with_smem(tps_sample_kernel<E, 1024, 1>, &attr_done[0], 1024, smem, a.m * cs, st, cs, max_smem, a);
+  return launch_with_smem(tps_sample_kernel<E, 256, 4>, &attr_done[1], 256, smem, a.m * cs, st, cs, max_smem, a);
+}
+
 int launch_sample(const SampleArgs& a, int num_sms, cudaStream_t st) {
   int cs = 1;
   while (cs < 8 && a.V > cs * 16384) cs *= 2;
@@ -514,11 +525,7 @@ int launch_sample(const SampleArgs& a, int num_sms, cudaStream_t st) {
   if (static_cast<long long>(a.m) * cs > 0x7fffffffLL) return -6;
   SampleArgs b = a;
   b.slice = ((a.V + cs - 1) / cs + 7) / 8 * 8;
-  const int smem = sample_smem_bytes(b.slice), max_smem = sample_smem_bytes(static_cast<int>(kSampleMaxVocab / 8));
-  static unsigned long long attr_done[2] = {0ull, 0ull};
-  if (static_cast<long long>(a.m) * cs <= num_sms && b.slice > 2048)
-    return launch_with_smem(tps_sample_kernel<1024, 1>, &attr_done[0], 1024, smem, a.m * cs, st, cs, max_smem, b);
-  return launch_with_smem(tps_sample_kernel<512, 2>, &attr_done[1], 512, smem, a.m * cs, st, cs, max_smem, b);
+  return a.f32 ? launch_sample_type<float>(b, cs, num_sms, st) : launch_sample_type<__nv_bfloat16>(b, cs, num_sms, st);
 }
 
 int launch_gemm(int swap, int bn, int dual, const CUtensorMap& tx, const CUtensorMap& tw, const GemmArgs& a,

@@ -9,22 +9,27 @@
 //
 // Every filter keeps a top part of the order (logit descending, index ascending), so a
 // row's filters are one threshold, the last kept token, and no sort of the row is needed.
-// One thread-block cluster holds a row in the shared memory of its CTAs (fp32, read once
-// from HBM) and finds the threshold from a histogram of up to 1024 equal bins over the
-// logits within 32 T of the maximum (what lies below has no weight): counts, and for top-p
-// weights as 16-bit numbers (a shift per octave of bins, so that a bin's sum keeps its
-// relative precision and fits 32 bits), whose truncation leaves one or two bins that can
-// hold the cut. The tokens of those bins go to the first CTA, which takes the cut from exact
-// sums. When the k largest fit its list of 1024 it takes both cuts there, and with
-// up to 256 of them it draws there too: each token finds its own place by comparing itself
-// with the others, which needs no sort and no further step of the cluster. Where the bin
-// holds more than the list (equal logits, one far outlier that stretches the bins), the
-// threshold is found bit by bit from passes over shared memory.
+// One thread-block cluster holds a row in the shared memory of its CTAs (in its own type,
+// read once from HBM) and finds the threshold in steps that end in a short list:
+//  - top-k: each thread has kept the largest logit of its part of the row. The k-th largest
+//    of those is a lower bound of the k-th largest logit, so their histogram (an entry per
+//    thread, not per token) gives a bin down to which all k lie, with few others.
+//  - top-p: a histogram of the weights of all tokens, as 16-bit numbers with a shift per
+//    octave of bins, so that a bin's 32-bit sum keeps its relative precision. It tells the
+//    bin of the cut but for roundings; exact sums tell in the next step whether it is, or
+//    the one beside it.
+// The tokens of those bins go to a list in the first CTA, which takes the cut from exact sums,
+// for top-k that of top-p too, and with up to 256 tokens it draws there: each token finds
+// its own place by comparing itself with the others, without a sort. Bins are equal parts
+// of the logits within 32 T of the maximum (what lies below has no weight). Where they hold
+// more than the list (equal logits, one far outlier that stretches them), the threshold is
+// found bit by bit from passes over shared memory.
 //
-// Bound by latency for few rows (six cluster barriers of about a microsecond) and by the
-// 64-bit exponentials and the passes over shared memory for many.
+// Bound by latency for few rows (five cluster barriers of about a microsecond), and by the
+// 64-bit exponentials and the shared-memory atomics of the weight histogram for many.
 #pragma once
 
+#include <cstddef>
 #include <cstdint>
 
 namespace tps {
@@ -33,7 +38,7 @@ typedef unsigned long long u64;
 
 constexpr int kSampleMaxWarps = 32;
 constexpr int kSampleBins = 1024;
-constexpr int kSampleList = 1024;              // entries of the candidate list, which overlays the histogram
+constexpr int kSampleList = 1024;              // entries of the candidate list, whose second half overlays the histogram
 constexpr u64 kSampleOne = 1ull << 44;         // weight of the largest logit
 constexpr int kSampleSmall = 256;              // kept tokens that the first CTA draws from by itself
 
@@ -42,18 +47,24 @@ __device__ __forceinline__ uint32_t atomic_add_cluster_u32(uint32_t addr, uint32
   asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(v) : "r"(addr), "r"(x) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
+// N consecutive words of another CTA's shared memory (N = 1 or 4).
+template <int N>
+__device__ __forceinline__ void ld_cluster(uint32_t addr, uint32_t (&v)[N]) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
+  else
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v[0]) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
-// Unsigned key with the order of the floats (NaN and -0 do not occur: sample_clean).
+// Unsigned key with the order of the floats, -0 as +0 (never called with a NaN).
 __device__ __forceinline__ uint32_t sample_key(float x) {
-  const uint32_t u = __float_as_uint(x);
+  const uint32_t u = __float_as_uint(x + 0.0f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 __device__ __forceinline__ float sample_unkey(uint32_t k) {
@@ -62,8 +73,24 @@ __device__ __forceinline__ float sample_unkey(uint32_t k) {
 __device__ __forceinline__ u64 sample_rank(float x, int i) {
   return static_cast<u64>(sample_key(x)) << 32 | (0xffffffffu - static_cast<uint32_t>(i));
 }
-// A NaN logit is never drawn; -0 equals +0.
-__device__ __forceinline__ float sample_clean(float x) { return x == x ? x + 0.0f : -INFINITY; }
+
+// Four consecutive logits of a row part in shared memory, held in the type that they came in.
+__device__ __forceinline__ void sample_get4(const float* xs, int v, float (&x)[4]) {
+  const float4 q = reinterpret_cast<const float4*>(xs)[v];
+  x[0] = q.x, x[1] = q.y, x[2] = q.z, x[3] = q.w;
+}
+__device__ __forceinline__ void sample_get4(const __nv_bfloat16* xs, int v, float (&x)[4]) {
+  const uint2 q = reinterpret_cast<const uint2*>(xs)[v];
+  x[0] = __uint_as_float(q.x << 16), x[1] = __uint_as_float(q.x & 0xffff0000u);
+  x[2] = __uint_as_float(q.y << 16), x[3] = __uint_as_float(q.y & 0xffff0000u);
+}
+__device__ __forceinline__ void sample_put4(float* xs, int v, const float (&x)[4]) {
+  reinterpret_cast<float4*>(xs)[v] = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void sample_put4(__nv_bfloat16* xs, int v, const float (&x)[4]) {   // bf16 values: exact
+  reinterpret_cast<uint2*>(xs)[v] =
+      make_uint2(__float_as_uint(x[0]) >> 16 | __float_as_uint(x[1]), __float_as_uint(x[2]) >> 16 | __float_as_uint(x[3]));
+}
 
 struct SampleRow {             // one row's parameters, the same in every CTA of its cluster
   double mx, c;                // largest logit; log2(e) / T
@@ -76,8 +103,8 @@ struct SampleRow {             // one row's parameters, the same in every CTA of
 // exp((x - mx) / T) in units of 2^-44, without a branch: 2^-y with y = (mx - x) log2(e) / T =
 // n + f, f in [-1/2, 1/2], 2^-f as its Taylor sum to (f ln 2)^9 / 9! (the rest is below
 // 2^-37), the power of two put into the exponent field, and the integer read from the low
-// bits after adding 2^52. The largest logit gives exactly 2^44; a y above 46 counts as 46,
-// whose weight rounds to 0.
+// bits after adding 2^52. The largest logit gives exactly 2^44; a y above 46 (or a NaN)
+// counts as 46, whose weight rounds to 0: the weight of -inf and of NaN.
 __device__ __forceinline__ u64 sample_weight(float x, const SampleRow& r) {
   const double y = fmin((r.mx - static_cast<double>(x)) * r.c, 46.0);
   const double t = y + 6755399441055744.0;                  // 1.5 * 2^52: y rounded to an integer, in the low bits
@@ -105,11 +132,13 @@ __device__ __forceinline__ int sample_bin(float x, const SampleRow& r) {
 // Weights of bin b are below 2^(16 + shift): the bin spans less than one octave of weights.
 __device__ __forceinline__ int sample_shift(int b, const SampleRow& r) { return max(0, 29 - (b >> r.octave)); }
 
+enum { SAMPLE_CUT, SAMPLE_DRAWN, SAMPLE_SHORT, SAMPLE_DOWN, SAMPLE_UP };   // threshold C; row finished; list too
+                                                                           // short; the cut is in a bin before / behind
 // What the first CTA tells the others about the next step (one copy per CTA).
 struct SampleCmd {
   int lo, hi;                  // bins whose tokens are listed
-  int n;                       // their number; -1: too many (bit by bit); -2: no cut
-  int drawn;                   // the row is finished
+  int skip;                    // nothing to list: 1 the cut keeps everything
+  int result;                  // after the list: one of SAMPLE_*
   u64 C;                       // the last kept token's rank
   u64 total;                   // top-k: tokens above the list; top-p: the weight of all
 };
@@ -119,13 +148,13 @@ struct SampleSmem {
   u64 part[2][8];              // values that the CTAs of the cluster exchange, two in turn
   u64 top[8];
   SampleCmd cmd;
-  int listed;                  // first CTA: list entries handed out to the CTAs
-  int place;                   // next free entry of this CTA's
+  int listed;                  // first CTA: list entries handed out
+  int unused;
   float fred[2 * kSampleMaxWarps];
 };
 
 constexpr int kSampleHead = (static_cast<int>(sizeof(SampleSmem)) + 15) / 16 * 16;
-constexpr int sample_smem_bytes(int slice) { return kSampleHead + kSampleBins * 8 + slice * 4; }
+constexpr int sample_smem_bytes(int slice, int f32) { return kSampleHead + kSampleBins * 8 + slice * (f32 ? 4 : 2); }
 
 template <class T, class Op>
 __device__ __forceinline__ T sample_warp_reduce(T v, Op op) {
@@ -165,17 +194,17 @@ __device__ __forceinline__ u64 sample_block_scan(u64 v, u64& total, SampleSmem& 
   return __shfl_sync(0xffffffffu, ws - w, warp) + incl - v;
 }
 
-template <int THREADS, int CTAS>
+template <class E, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleArgs a) {
   constexpr int WARPS = THREADS / 32;
   constexpr int BPT = kSampleBins / THREADS;     // bins (and list entries) per thread
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SampleSmem& s = *reinterpret_cast<SampleSmem*>(smem_raw);
-  uint32_t* cnt = reinterpret_cast<uint32_t*>(smem_raw + kSampleHead);
-  uint32_t* mass = cnt + kSampleBins;
-  u64* list = reinterpret_cast<u64*>(cnt);
-  float* xs = reinterpret_cast<float*>(mass + kSampleBins);
-  static_assert(kSampleList <= kSampleBins && 2 * kSampleSmall <= THREADS, "shared memory layout");
+  u64* list = reinterpret_cast<u64*>(smem_raw + kSampleHead);
+  uint32_t* hist = reinterpret_cast<uint32_t*>(list + kSampleList / 2);
+  E* xs = reinterpret_cast<E*>(hist + kSampleBins);
+  static_assert(kSampleList * 8 == kSampleBins * 8 && kSampleSmall <= THREADS && (BPT == 1 || BPT == 4),
+                "shared memory layout");
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cs = static_cast<int>(cluster_nctarank()), cr = static_cast<int>(cluster_ctarank());
@@ -194,44 +223,33 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
     return t;
   };
   griddep_wait();
+  const float T = a.temperature ? a.temperature[row] : 1.0f;
+  const float pf = a.top_p ? a.top_p[row] : 1.0f;
+  const float qf = a.min_p ? a.min_p[row] : 0.0f;
+  const int top_k = a.top_k ? a.top_k[row] : 0;
+  const double u = fmin(fmax(static_cast<double>(a.u[row]), 0.0), 1.0);    // NaN: 0
+  const bool greedy = !(T >= 7.888609e-31f);   // 2^-100: the bins' scale stays finite
 
   // ------------------------------------------------ the row into shared memory, its largest and smallest logit
-  float mx = -INFINITY, mn = INFINITY;
-  auto take = [&](float x) {
-    mx = fmaxf(mx, x);
-    mn = fminf(mn, x > -INFINITY ? x : INFINITY);
-  };
-  if (a.f32) {
-    const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) +
-                                                        static_cast<long long>(row) * a.V + i0);
+  float mx = -INFINITY, mn = INFINITY;         // neither takes a NaN
+  const E* src = static_cast<const E*>(a.logits) + static_cast<long long>(row) * a.V + i0;
+  constexpr int EPV = 16 / sizeof(E);
 #pragma unroll 8
-    for (int v = tid; v < n / 4; v += THREADS) {
-      float4 x = __ldcs(src + v);
-      x = make_float4(sample_clean(x.x), sample_clean(x.y), sample_clean(x.z), sample_clean(x.w));
-      reinterpret_cast<float4*>(xs)[v] = x;
-      take(x.x), take(x.y), take(x.z), take(x.w);
-    }
-  } else {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.logits) +
-                                                      static_cast<long long>(row) * a.V + i0);
-#pragma unroll 4
-    for (int v = tid; v < n / 8; v += THREADS) {
-      const uint4 b = __ldcs(src + v);
-      const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-      float x[8];
+  for (int v = tid; v < n / EPV; v += THREADS) {
+    const uint4 q = __ldcs(reinterpret_cast<const uint4*>(src) + v);
+    reinterpret_cast<uint4*>(xs)[v] = q;
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[2 * j] = sample_clean(__uint_as_float(w[j] << 16));
-        x[2 * j + 1] = sample_clean(__uint_as_float(w[j] & 0xffff0000u));
-      }
-      reinterpret_cast<float4*>(xs)[2 * v] = make_float4(x[0], x[1], x[2], x[3]);
-      reinterpret_cast<float4*>(xs)[2 * v + 1] = make_float4(x[4], x[5], x[6], x[7]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) take(x[j]);
+    for (int j = 0; j < 4; ++j) {
+      const float x = __uint_as_float(EPV == 4 ? w[j] : w[j] & 0xffff0000u);
+      const float y = EPV == 4 ? x : __uint_as_float(w[j] << 16);
+      mx = fmaxf(fmaxf(mx, x), y);
+      mn = fminf(fminf(mn, x), y);
     }
   }
-  for (int j = tid; j < kSampleBins; j += THREADS) cnt[j] = mass[j] = 0;
-  if (tid == 0) s.listed = s.cmd.drawn = 0;
+  float most = mx;                             // this thread's largest
+  for (int j = tid; j < kSampleBins; j += THREADS) hist[j] = 0;
+  if (tid == 0) s.listed = 0;
   mx = sample_warp_reduce(mx, [](float x, float y) { return fmaxf(x, y); });
   mn = sample_warp_reduce(mn, [](float x, float y) { return fminf(x, y); });
   if (lane == 0) s.fred[warp] = mx, s.fred[WARPS + warp] = mn;
@@ -241,6 +259,21 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
     mx = fmaxf(mx, s.fred[w]);
     mn = fminf(mn, s.fred[WARPS + w]);
   }
+  if (mn == -INFINITY && mx > -INFINITY) {     // masked logits: the smallest of the others
+    mn = INFINITY;
+    for (int v = tid; v < n / 4; v += THREADS) {
+      float x[4];
+      sample_get4(xs, v, x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mn = x[j] > -INFINITY ? fminf(mn, x[j]) : mn;
+    }
+    mn = sample_warp_reduce(mn, [](float x, float y) { return fminf(x, y); });
+    __syncthreads();
+    if (lane == 0) s.fred[warp] = mn;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) mn = fminf(mn, s.fred[w]);
+  }
   if (tid < cs)
     st_cluster_u64(remote(&s.top[cr], tid), static_cast<u64>(__float_as_uint(mx)) << 32 | __float_as_uint(mn));
   cluster_sync_all();
@@ -249,20 +282,15 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
     mn = fminf(mn, __uint_as_float(static_cast<uint32_t>(s.top[r])));
   }
 
-  const float T = a.temperature ? a.temperature[row] : 1.0f;
-  const float pf = a.top_p ? a.top_p[row] : 1.0f;
-  const int top_k = a.top_k ? a.top_k[row] : 0;
-  const double u = fmin(fmax(static_cast<double>(a.u[row]), 0.0), 1.0);    // NaN: 0
-  const bool greedy = !(T > 0.0f);
   float cx = -INFINITY;                        // kept: x > cx, or x == cx and index <= ci (and min_p)
   int ci = -1;
-  auto each = [&](auto f) {                    // every kept token of this CTA (never a logit of -inf)
+  auto keeps = [&](float x, int i) { return x > cx || (x == cx && i <= ci); };
+  auto each = [&](auto f) {                    // every token of this CTA
     for (int v = tid; v < n / 4; v += THREADS) {
-      const float4 q = reinterpret_cast<const float4*>(xs)[v];
-      const float x[4] = {q.x, q.y, q.z, q.w};
+      float x[4];
+      sample_get4(xs, v, x);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (x[j] > cx || (x[j] == cx && i0 + 4 * v + j <= ci)) f(x[j], i0 + 4 * v + j);
+      for (int j = 0; j < 4; ++j) f(x[j], i0 + 4 * v + j);
     }
   };
   if (greedy || mx == -INFINITY) {             // the same in the whole cluster
@@ -286,21 +314,26 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
     return;
   }
   if (mx == INFINITY) {                        // +inf logits share the weight: as 0 among -inf
-    for (int j = tid; j < n; j += THREADS) xs[j] = xs[j] == INFINITY ? 0.0f : -INFINITY;
+    for (int v = tid; v < n / 4; v += THREADS) {
+      float x[4];
+      sample_get4(xs, v, x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = x[j] == INFINITY ? 0.0f : -INFINITY;
+      sample_put4(xs, v, x);
+    }
     mx = mn = 0.0f;
+    most = most == INFINITY ? 0.0f : -INFINITY;
     __syncthreads();
   }
   SampleRow r;
   r.mxf = mx;
   r.mx = static_cast<double>(mx);
   r.c = 1.4426950408889634 / static_cast<double>(T);
-  r.q = 0;
-  if (a.min_p && a.min_p[row] > 0.0f)
-    r.q = static_cast<u64>(ceil(fmin(static_cast<double>(a.min_p[row]), 1.0) * static_cast<double>(kSampleOne)));
-  // 2^octave bins per factor of 2: as many as keep the range within the bins
-  const double span = fmin((r.mx - static_cast<double>(mn)) * r.c, 46.2);   // in factors of 2; 46.2 = 32 log2(e)
-  const int octave = span > 0.0 ? min(100, ilogb(static_cast<double>(kSampleBins - 1) / span)) : 0;   // at least 4
-  r.bin_scale = static_cast<float>(fmin(scalbn(r.c, octave), 3e38));
+  r.q = qf > 0.0f ? static_cast<u64>(ceil(fmin(static_cast<double>(qf), 1.0) * static_cast<double>(kSampleOne))) : 0;
+  // 2^octave bins per factor of 2 in the weight: as many as keep the range within the bins
+  const float span = fminf((mx - mn) * static_cast<float>(r.c), 46.2f);    // in factors of 2; 46.2 = 32 log2(e)
+  const int octave = span > 0.0f ? min(100, ilogbf(static_cast<float>(kSampleBins - 1) / span)) : 0;   // at least 4
+  r.bin_scale = scalbnf(static_cast<float>(r.c), octave);
   r.octave = min(octave, 31);
   const double p = static_cast<double>(pf);
   auto survives = [&](u64 w) { return w >= r.q; };         // min_p
@@ -320,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
       const u64 c = t | (1ull << bit);
       u64 v = 0;
       each([&](float x, int i) {
-        if (sample_rank(x, i) >= c) v += by_weight ? sample_weight(x, r) : 1ull;
+        if (keeps(x, i) && sample_rank(x, i) >= c) v += by_weight ? sample_weight(x, r) : 1ull;
       });
       v = cluster_all(sample_block_sum<THREADS>(v, s));
       if (by_weight ? (v > 0 && static_cast<double>(v) >= target) : v >= want) t = c;
@@ -328,89 +361,73 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
     return t;
   };
   auto set_threshold = [&](u64 rank) {
-    const float x = sample_unkey(static_cast<uint32_t>(rank >> 32));
-    const int i = static_cast<int>(0xffffffffu - static_cast<uint32_t>(rank));
-    if (x > cx || (x == cx && i < ci)) cx = x, ci = i;
+    cx = sample_unkey(static_cast<uint32_t>(rank >> 32));    // always within the tokens kept so far
+    ci = static_cast<int>(0xffffffffu - static_cast<uint32_t>(rank));
   };
 
   // One cut of the kept tokens: the k first of them (k > 0), or those that reach the share p
-  // of their weight. With by_p the cut to k may take p, or the draw, in the same step:
-  // returns what is left to do.
-  enum { NOTHING, DRAW, CUT_P };
-  auto cut = [&](int k, bool by_p) -> int {
+  // of their weight. With by_p the cut to k may take p, or the draw, in the same step.
+  // by_thread: k from the threads' largest logits, of which the row has more than k. Returns
+  // what is left to do.
+  enum { NOTHING, DRAW, CUT_P, RETRY };
+  auto cut = [&](int k, bool by_p, bool by_thread) -> int {
     u64 sum = 0;
-    if (k > 0) {
-      each([&](float x, int) { atomicAdd(cnt + sample_bin(x, r), 1u); });
+    if (k > 0 && by_thread) {
+      if (most > -INFINITY) atomicAdd(hist + sample_bin(most, r), 1u);
+      __syncthreads();
+    } else if (k > 0) {
+      each([&](float x, int i) {
+        if (keeps(x, i)) atomicAdd(hist + sample_bin(x, r), 1u);
+      });
       __syncthreads();
     } else {
-      each([&](float x, int) {
+      each([&](float x, int i) {
         const int b = sample_bin(x, r);
         const u64 w = sample_weight(x, r);
-        sum += w;
-        atomicAdd(cnt + b, 1u);
-        atomicAdd(mass + b, static_cast<uint32_t>(w >> sample_shift(b, r)));
+        if (keeps(x, i)) {
+          sum += w;
+          const int sh = sample_shift(b, r);
+          const uint32_t m = static_cast<uint32_t>((w + ((1ull << sh) >> 1)) >> sh);
+          if (m) atomicAdd(hist + b, m);
+        }
       });
       sum = sample_block_sum<THREADS>(sum, s);
     }
     const u64 total = cluster_all(sum);
     if (cr == 0) {
-      // BPT bins per thread over the cluster: what lies before each, in tokens or in weight (a
-      // lower and an upper bound)
-      u64 c[BPT], lo[BPT], hi[BPT], lsum = 0, hsum = 0, all, unused;
+      // BPT bins per thread over the cluster: what lies before each, in tokens or in weight
+      u64 v[BPT], sum = 0, all;
+      uint32_t h[8][BPT];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < cs) ld_cluster<BPT>(remote(hist + tid * BPT, q), h[q]);
 #pragma unroll
       for (int j = 0; j < BPT; ++j) {
-        const int b = tid * BPT + j;
-        u64 m = 0;
-        c[j] = 0;
+        v[j] = 0;
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          if (q < cs) {
-            c[j] += ld_cluster_u32(remote(cnt + b, q));
-            if (k == 0) m += ld_cluster_u32(remote(mass + b, q));
-          }
-        lo[j] = k > 0 ? c[j] : m << sample_shift(b, r);
-        hi[j] = k > 0 ? c[j] : (m + c[j]) << sample_shift(b, r);
-        lsum += lo[j];
-        hsum += hi[j];
+          if (q < cs) v[j] += h[q][j];
+        if (k == 0) v[j] <<= sample_shift(tid * BPT + j, r);
+        sum += v[j];
       }
-      u64 lb = sample_block_scan<THREADS>(lsum, all, s);
-      u64 hb = k > 0 ? lb : sample_block_scan<THREADS>(hsum, unused, s);
+      u64 before = sample_block_scan<THREADS>(sum, all, s);
       if (tid == 0) {
-        s.cmd.lo = 0;                          // set below by the bins that the cut can lie in
-        s.cmd.hi = kSampleBins - 1;
-        s.cmd.n = k > 0 && static_cast<u64>(k) >= all ? -2 : 0;
+        s.cmd.lo = s.cmd.hi = k > 0 ? kSampleBins - 1 : 0;
+        s.cmd.skip = k > 0 && !by_thread && static_cast<u64>(k) >= all;
         s.cmd.total = total;
       }
       __syncthreads();
-      const double target = k > 0 ? static_cast<double>(k) : p * static_cast<double>(total);
-#pragma unroll
-      for (int j = 0; j < BPT; ++j) {          // the first bin that may reach the target, and the first that must
-        if (static_cast<double>(hb) < target && static_cast<double>(hb + hi[j]) >= target) s.cmd.lo = tid * BPT + j;
-        if (static_cast<double>(lb) < target && static_cast<double>(lb + lo[j]) >= target) {
-          s.cmd.hi = tid * BPT + j;
-          if (k > 0) s.cmd.total = lb;
-        }
-        hb += hi[j];
-        lb += lo[j];
-      }
-      if (!(target > 0.0) && tid == 0) s.cmd.hi = 0;       // the largest logit alone: bin 0 has it
-      __syncthreads();
-      u64 listed = 0, before = 0;
+      // the bin in which the running value reaches the target (rounded weights: of their own total)
+      const double target = k > 0 ? static_cast<double>(k) : p * static_cast<double>(all);
 #pragma unroll
       for (int j = 0; j < BPT; ++j) {
-        const int b = tid * BPT + j;
-        if (b >= s.cmd.lo && b <= s.cmd.hi) listed += c[j];
-        if (b < s.cmd.lo) before += c[j];
-      }
-      listed = sample_block_sum<THREADS>(listed, s);
-      before = sample_block_sum<THREADS>(before, s);
-      if (tid == 0 && s.cmd.n == 0) {
-        if (k > 0 && before + listed <= kSampleList) {     // every kept token fits the list
-          s.cmd.lo = 0;
-          s.cmd.total = 0;
-          listed += before;
+        if (static_cast<double>(before) < target && static_cast<double>(before + v[j]) >= target) {
+          const bool from0 = k > 0 && (by_thread || before + v[j] <= kSampleList);   // the k largest may fit the list
+          s.cmd.lo = from0 ? 0 : tid * BPT + j;
+          s.cmd.hi = tid * BPT + j;
+          if (k > 0) s.cmd.total = from0 ? 0 : before;
         }
-        s.cmd.n = listed > kSampleList ? -1 : static_cast<int>(listed);
+        before += v[j];
       }
       __syncthreads();
       // the command to the other CTAs
@@ -418,128 +435,150 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
         for (int q = 1; q < cs; ++q)
           st_cluster_u64(remote(reinterpret_cast<u64*>(&s.cmd) + tid, q), reinterpret_cast<const u64*>(&s.cmd)[tid]);
     }
-    cluster_sync_all();                        // also: the first CTA has read the histograms
-    const SampleCmd cmd = s.cmd;
+    cluster_sync_all();                        // also: the histograms have been read, the list may overwrite the first one
+    SampleCmd cmd = s.cmd;
     const int after = by_p && k > 0 ? CUT_P : DRAW;
-    if (cmd.n < 0) {
-      if (cmd.n == -1)
-        set_threshold(k > 0 ? bisect(false, static_cast<u64>(k), 0.0)
-                            : bisect(true, 0, p * static_cast<double>(cmd.total)));
-      for (int j = tid; j < kSampleBins; j += THREADS) cnt[j] = 0, mass[j] = 0;
-      __syncthreads();
-      return after;
-    }
-    // this CTA's place in the list: as many entries as its own histogram says
-    u64 c = 0;
-    for (int b = cmd.lo + tid; b <= cmd.hi; b += THREADS) c += cnt[b];
-    c = sample_block_sum<THREADS>(c, s);
-    if (tid == 0)
-      s.place = c ? static_cast<int>(atomic_add_cluster_u32(remote(&s.listed, 0), static_cast<uint32_t>(c))) : 0;
-    cluster_sync_all();                        // every CTA has read its histogram: the list may overwrite the first one's
-    u64 above = 0;                             // weight above the list
-    if (c || k == 0)
-      each([&](float x, int i) {
-        const int b = sample_bin(x, r);
-        if (b >= cmd.lo && b <= cmd.hi) st_cluster_u64(remote(list + atomicAdd(&s.place, 1), 0), sample_rank(x, i));
-        else if (k == 0 && b < cmd.lo) above += sample_weight(x, r);
-      });
-    if (cr > 0)                                // for a second cut
-      for (int j = tid; j < kSampleBins; j += THREADS) cnt[j] = mass[j] = 0;
-    above = cluster_all(k == 0 ? sample_block_sum<THREADS>(above, s) : 0);
     const bool whole = k > 0 && cmd.lo == 0;   // the list begins at the top
-    if (cr == 0) {
-      const int len = cmd.n;
-      if (whole && len <= kSampleSmall) {
-        // THREADS / 256 threads per token e: how many tokens come before it and their weight, then the
-        // weight of the kept tokens up to it in vocabulary order.
-        constexpr int TPE = THREADS / kSampleSmall;
-        const int e = tid / TPE, half = tid % TPE;
-        const u64 re = e < len ? list[e] : 0;
-        const u64 we = e < len ? sample_weight(sample_unkey(static_cast<uint32_t>(re >> 32)), r) : 0;
-        u64* w = list + kSampleSmall;          // weights, by list entry (each pair writes its own)
-        if (half == 0) w[e] = we;
+    auto tell = [&](int result) {              // first CTA: what comes of the list
+      if (tid < cs) st_cluster_u64(remote(&s.cmd.skip, tid), static_cast<u64>(result) << 32);
+    };
+    static_assert(offsetof(SampleCmd, skip) % 8 == 0 && offsetof(SampleCmd, result) == offsetof(SampleCmd, skip) + 4,
+                  "one 64-bit store");
+    int result = SAMPLE_CUT;
+    do {
+      u64 above = 0;                             // weight above the list
+      if (!cmd.skip)
+        each([&](float x, int i) {
+          if (!keeps(x, i)) return;
+          const int b = sample_bin(x, r);
+          if (b >= cmd.lo && b <= cmd.hi) {
+            const uint32_t at = atomic_add_cluster_u32(remote(&s.listed, 0), 1u);
+            if (at < kSampleList) st_cluster_u64(remote(list + at, 0), sample_rank(x, i));
+          } else if (k == 0 && b < cmd.lo) {
+            above += sample_weight(x, r);
+          }
+        });
+      if (cr > 0)                                // for another cut
+        for (int j = tid; j < kSampleBins; j += THREADS) hist[j] = 0;
+      above = cluster_all(k == 0 ? sample_block_sum<THREADS>(above, s) : 0);
+      if (cmd.skip) {
+        if (cr == 0)
+          for (int j = tid; j < kSampleBins; j += THREADS) hist[j] = 0;
         __syncthreads();
-        int place = 0;
-        u64 larger = 0;
-        for (int j = half; j < len; j += TPE)
-          if (list[j] > re) ++place, larger += w[j];
+        return after;
+      }
+      if (cr == 0) {
+        const int len = s.listed;
+        if (len > kSampleList) {
+          tell(SAMPLE_SHORT);
+        } else if (whole && len <= kSampleSmall) {
+          // THREADS / 256 threads per token e: how many tokens come before it and their weight, then the
+          // weight of the kept tokens up to it in vocabulary order.
+          constexpr int TPE = THREADS / kSampleSmall;
+          const int e = tid / TPE, half = tid % TPE;
+          const u64 re = e < len ? list[e] : 0;
+          const u64 we = e < len ? sample_weight(sample_unkey(static_cast<uint32_t>(re >> 32)), r) : 0;
+          u64* w = list + kSampleSmall;          // weights, by list entry (each pair writes its own)
+          if (half == 0) w[e] = we;
+          __syncthreads();
+          int place = 0;
+          u64 larger = 0;
+          for (int j = half; j < len; j += TPE)
+            if (list[j] > re) ++place, larger += w[j];
 #pragma unroll
-        for (int o = 1; o < TPE; o <<= 1) {
-          place += __shfl_xor_sync(0xffffffffu, place, o);
-          larger += __shfl_xor_sync(0xffffffffu, larger, o);
-        }
-        bool in = e < len && place < k;
-        if (by_p) {
-          const u64 wk = sample_block_sum<THREADS>(in && half == 0 ? we : 0, s);
-          in = in && (place == 0 || static_cast<double>(larger) < p * static_cast<double>(wk));
-        }
-        in = in && survives(we);
-        __syncthreads();
-        if (half == 0) w[e] = in ? we : 0;
-        const u64 tot = sample_block_sum<THREADS>(in && half == 0 ? we : 0, s);
-        const uint32_t ie = static_cast<uint32_t>(re);           // ~index: larger is earlier
-        u64 upto = 0;
-        for (int j = half; j < len; j += TPE)
-          if (static_cast<uint32_t>(list[j]) >= ie) upto += w[j];
+          for (int o = 1; o < TPE; o <<= 1) {
+            place += __shfl_xor_sync(0xffffffffu, place, o);
+            larger += __shfl_xor_sync(0xffffffffu, larger, o);
+          }
+          bool in = e < len && place < k;
+          if (by_p) {
+            const u64 wk = sample_block_sum<THREADS>(in && half == 0 ? we : 0, s);
+            in = in && (place == 0 || static_cast<double>(larger) < p * static_cast<double>(wk));
+          }
+          in = in && survives(we);
+          __syncthreads();
+          if (half == 0) w[e] = in ? we : 0;
+          const u64 tot = sample_block_sum<THREADS>(in && half == 0 ? we : 0, s);
+          const uint32_t ie = static_cast<uint32_t>(re);           // ~index: larger is earlier
+          u64 upto = 0;
+          for (int j = half; j < len; j += TPE)
+            if (static_cast<uint32_t>(list[j]) >= ie) upto += w[j];
 #pragma unroll
-        for (int o = 1; o < TPE; o <<= 1) upto += __shfl_xor_sync(0xffffffffu, upto, o);
-        const u64 t = goal(tot);
-        if (in && half == 0 && upto > t && upto - we <= t) draw(static_cast<int>(0xffffffffu - ie), we, tot);
-        if (tid < cs) {
-          SampleCmd done = cmd;
-          done.drawn = 1;
-          st_cluster_u64(remote(&s.cmd.n, tid), reinterpret_cast<const u64*>(&done)[1]);
-        }
-      } else {
-        int m = 32;                            // bitonic sort, descending, padded with zeros
-        while (m < len) m <<= 1;
-        for (int j = len + tid; j < m; j += THREADS) list[j] = 0;
-        __syncthreads();
-        for (int size = 2; size <= m; size <<= 1)
-          for (int d = size >> 1; d > 0; d >>= 1) {
-            for (int j = tid; j < m / 2; j += THREADS) {
-              const int lo = 2 * j - (j & (d - 1)), hi = lo + d;
-              const u64 x = list[lo], y = list[hi];
-              if ((x < y) == ((lo & size) == 0)) list[lo] = y, list[hi] = x;
+          for (int o = 1; o < TPE; o <<= 1) upto += __shfl_xor_sync(0xffffffffu, upto, o);
+          const u64 t = goal(tot);
+          if (in && half == 0 && upto > t && upto - we <= t) draw(static_cast<int>(0xffffffffu - ie), we, tot);
+          tell(SAMPLE_DRAWN);
+        } else {
+          int m = 32;                            // bitonic sort, descending, padded with zeros
+          while (m < len) m <<= 1;
+          for (int j = len + tid; j < m; j += THREADS) list[j] = 0;
+          __syncthreads();
+          for (int size = 2; size <= m; size <<= 1)
+            for (int d = size >> 1; d > 0; d >>= 1) {
+              for (int j = tid; j < m / 2; j += THREADS) {
+                const int lo = 2 * j - (j & (d - 1)), hi = lo + d;
+                const u64 x = list[lo], y = list[hi];
+                if ((x < y) == ((lo & size) == 0)) list[lo] = y, list[hi] = x;
+              }
+              __syncthreads();
             }
-            __syncthreads();
-          }
-        const int kk = k > 0 ? k - static_cast<int>(cmd.total) : len;   // entries that may stay
-        int last = kk - 1;                     // the last kept one
-        if (k == 0 || (whole && by_p)) {
-          u64 w[BPT], sum = 0, tot;            // BPT entries per thread: the weight before each
+          const int kk = k > 0 ? k - static_cast<int>(cmd.total) : len;   // entries that may stay
+          int last = kk - 1;                     // the last kept one
+          int found = SAMPLE_CUT;
+          if (k == 0 || (whole && by_p)) {
+            u64 w[BPT], sum = 0, tot;            // BPT entries per thread: the weight before each
 #pragma unroll
-          for (int j = 0; j < BPT; ++j) {
-            w[j] = tid * BPT + j < kk
-                       ? sample_weight(sample_unkey(static_cast<uint32_t>(list[tid * BPT + j] >> 32)), r) : 0;
-            sum += w[j];
-          }
-          u64 before = sample_block_scan<THREADS>(sum, tot, s) + above;
-          const double target = p * static_cast<double>(k == 0 ? cmd.total : tot);
-          u64 kept = 0;
+            for (int j = 0; j < BPT; ++j) {
+              w[j] = tid * BPT + j < kk
+                         ? sample_weight(sample_unkey(static_cast<uint32_t>(list[tid * BPT + j] >> 32)), r) : 0;
+              sum += w[j];
+            }
+            u64 before = sample_block_scan<THREADS>(sum, tot, s) + above;
+            const double target = p * static_cast<double>(k == 0 ? cmd.total : tot);
+            u64 kept = 0;
 #pragma unroll
-          for (int j = 0; j < BPT; ++j) {
-            kept += tid * BPT + j < kk && static_cast<double>(before) < target;
-            before += w[j];
+            for (int j = 0; j < BPT; ++j) {
+              kept += tid * BPT + j < kk && static_cast<double>(before) < target;
+              before += w[j];
+            }
+            last = max(static_cast<int>(sample_block_sum<THREADS>(kept, s)), 1) - 1;
+            if (k == 0 && cmd.lo > 0 && static_cast<double>(above) >= target) found = SAMPLE_DOWN;
+            else if (k == 0 && cmd.hi < kSampleBins - 1 && static_cast<double>(above + tot) < target) found = SAMPLE_UP;
           }
-          last = max(static_cast<int>(sample_block_sum<THREADS>(kept, s)), 1) - 1;
+          const u64 C = list[last];
+          __syncthreads();
+          if (tid < cs) st_cluster_u64(remote(&s.cmd.C, tid), C);
+          tell(found);
         }
-        const u64 C = list[last];
-        __syncthreads();
-        if (tid < cs) st_cluster_u64(remote(&s.cmd.C, tid), C);
-        for (int j = tid; j < kSampleBins; j += THREADS) cnt[j] = mass[j] = 0;
+        __syncthreads();                         // every thread has read `listed` and the list
+        for (int j = tid; j < kSampleBins; j += THREADS) hist[j] = 0;
         if (tid == 0) s.listed = 0;
       }
+      cluster_sync_all();
+      result = s.cmd.result;
+      const int move = result == SAMPLE_UP ? 1 : result == SAMPLE_DOWN ? -1 : 0;
+      cmd.lo += move;
+      cmd.hi += move;
+    } while (result >= SAMPLE_DOWN);           // ends: the exact sums order the bins
+    if (result == SAMPLE_DRAWN) return NOTHING;
+    if (result == SAMPLE_SHORT) {
+      if (k > 0 && by_thread) return RETRY;
+      set_threshold(k > 0 ? bisect(false, static_cast<u64>(k), 0.0)
+                          : bisect(true, 0, p * static_cast<double>(cmd.total)));
+      return after;
     }
-    cluster_sync_all();
-    if (s.cmd.drawn) return NOTHING;
     set_threshold(s.cmd.C);
     return whole ? DRAW : after;
   };
   const bool by_p = p < 1.0;
   int left = by_p ? CUT_P : DRAW;
-  if (top_k > 0 && top_k < a.V) left = cut(top_k, by_p);
-  if (left == CUT_P) left = cut(0, true);
+  if (top_k > 0 && top_k < a.V) {
+    // threads with a finite logit in the cluster: more than k of them, or count tokens
+    const u64 have = cluster_all(static_cast<u64>(__syncthreads_count(most > -INFINITY)));
+    left = have > static_cast<u64>(top_k) ? cut(top_k, by_p, true) : RETRY;
+    if (left == RETRY) left = cut(top_k, by_p, false);
+  }
+  if (left == CUT_P) left = cut(0, true, false);
   if (left == NOTHING) return;
 
   // ------------------------------------------------ the draw, in vocabulary order: a warp has a contiguous part
@@ -547,15 +586,19 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
   const int j0 = min(n, warp * per), j1 = min(n, j0 + per);
   auto kept = [&](float x, int j) -> u64 {
     const u64 w = sample_weight(x, r);
-    const bool in = x > cx || (x == cx && i0 + j <= ci);
-    return in && survives(w) ? w : 0ull;
+    return keeps(x, i0 + j) && survives(w) ? w : 0ull;
   };
   u64 mine = 0;
-  for (int j = j0 + 4 * lane; j < j1; j += 128) {
-    const float4 x = *reinterpret_cast<const float4*>(xs + j);
-    if (fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) >= cx)     // few lanes have any behind a filter
-      mine += (kept(x.x, j) + kept(x.y, j + 1)) + (kept(x.z, j + 2) + kept(x.w, j + 3));
-  }
+  auto part = [&](auto f) {
+    for (int j = j0 + 4 * lane; j < j1; j += 128) {
+      float x[4];
+      sample_get4(xs, j >> 2, x);
+      if (fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= cx)
+        mine += (f(x[0], j) + f(x[1], j + 1)) + (f(x[2], j + 2) + f(x[3], j + 3));
+    }
+  };
+  if (r.q > 0 || cx > -INFINITY) part(kept);
+  else part([&](float x, int) { return sample_weight(x, r); });
   mine = sample_warp_reduce(mine, [](u64 x, u64 y) { return x + y; });
   __syncthreads();
   if (lane == 0) s.red[warp] = mine;
@@ -576,7 +619,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
   const u64 target = goal(total);
   if (before <= target && target < before + mine) {
     for (int jb = j0; jb < j1; jb += 32) {
-      const u64 w = jb + lane < j1 ? kept(xs[jb + lane], jb + lane) : 0;
+      const u64 w = jb + lane < j1 ? kept(static_cast<float>(xs[jb + lane]), jb + lane) : 0;
       u64 incl = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
