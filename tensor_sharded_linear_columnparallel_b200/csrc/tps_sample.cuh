@@ -14,10 +14,10 @@
 //  - top-k: each thread has kept the largest logit of its part of the row. The k-th largest
 //    of those is a lower bound of the k-th largest logit, so their histogram (an entry per
 //    thread, not per token) gives a bin down to which all k lie, with few others.
-//  - top-p: a histogram of the weights of all tokens, as 16-bit numbers with a shift per
+//  - top-p: a histogram of fast approximate weights, as 16-bit numbers with a shift per
 //    octave of bins, so that a bin's 32-bit sum keeps its relative precision. It tells the
-//    bin of the cut but for roundings; exact sums tell in the next step whether it is, or
-//    the one beside it.
+//    bin of the cut but for roundings; the one pass that computes the exact weights, of all
+//    tokens and of those above the bin, tells whether it is that bin or the one beside it.
 // The tokens of those bins go to a list in the first CTA, which takes the cut from exact sums,
 // for top-k that of top-p too, and with up to 256 tokens it draws there: each token finds
 // its own place by comparing itself with the others, without a sort. Bins are equal parts
@@ -140,13 +140,14 @@ struct SampleCmd {
   int skip;                    // nothing to list: 1 the cut keeps everything
   int result;                  // after the list: one of SAMPLE_*
   u64 C;                       // the last kept token's rank
-  u64 total;                   // top-k: tokens above the list; top-p: the weight of all
+  u64 total;                   // top-k: tokens above the list
 };
 
 struct SampleSmem {
   u64 red[kSampleMaxWarps];
   u64 part[2][8];              // values that the CTAs of the cluster exchange, two in turn
-  u64 top[8];
+  u64 part2[2][8];
+  u64 top[8], have[8];
   SampleCmd cmd;
   int listed;                  // first CTA: list entries handed out
   int unused;
@@ -213,14 +214,22 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
   // address of the same place in CTA r of the cluster
   auto remote = [&](const void* p, int r) { return mapa_shared(smem_u32(p), static_cast<uint32_t>(r)); };
   int turn = 0;
-  // sum of one value per CTA, in every CTA (v the same in all threads of a CTA)
-  auto cluster_all = [&](u64 v) {
-    if (tid < cs) st_cluster_u64(remote(&s.part[turn][cr], tid), v);
+  // sums of two values per CTA, in every CTA (the same in all threads of a CTA)
+  auto cluster_all2 = [&](u64 v, u64& v2) {
+    if (tid < cs) {
+      st_cluster_u64(remote(&s.part[turn][cr], tid), v);
+      st_cluster_u64(remote(&s.part2[turn][cr], tid), v2);
+    }
     cluster_sync_all();
     u64 t = 0;
-    for (int r = 0; r < cs; ++r) t += s.part[turn][r];
+    v2 = 0;
+    for (int r = 0; r < cs; ++r) t += s.part[turn][r], v2 += s.part2[turn][r];
     turn ^= 1;
     return t;
+  };
+  auto cluster_all = [&](u64 v) {
+    u64 none = 0;
+    return cluster_all2(v, none);
   };
   griddep_wait();
   const float T = a.temperature ? a.temperature[row] : 1.0f;
@@ -274,10 +283,16 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) mn = fminf(mn, s.fred[w]);
   }
-  if (tid < cs)
+  // also: how many threads have a logit above -inf
+  const int finite = __syncthreads_count(most > -INFINITY);
+  if (tid < cs) {
     st_cluster_u64(remote(&s.top[cr], tid), static_cast<u64>(__float_as_uint(mx)) << 32 | __float_as_uint(mn));
+    st_cluster_u64(remote(&s.have[cr], tid), static_cast<u64>(finite));
+  }
   cluster_sync_all();
+  u64 have = 0;
   for (int r = 0; r < cs; ++r) {
+    have += s.have[r];
     mx = fmaxf(mx, __uint_as_float(static_cast<uint32_t>(s.top[r] >> 32)));
     mn = fminf(mn, __uint_as_float(static_cast<uint32_t>(s.top[r])));
   }
@@ -322,7 +337,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
       sample_put4(xs, v, x);
     }
     mx = mn = 0.0f;
-    most = most == INFINITY ? 0.0f : -INFINITY;
+    most = -INFINITY;
+    have = 0;                                  // top_k counts tokens
     __syncthreads();
   }
   SampleRow r;
@@ -346,9 +362,17 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
     if (a.out_logp) a.out_logp[row] = static_cast<float>(log(static_cast<double>(w) / static_cast<double>(total)));
   };
 
-  // Largest threshold at which `want` tokens (or, by weight, `target`) are kept, bit by bit.
-  auto bisect = [&](bool by_weight, u64 want, double target) {
+  // Largest threshold at which `want` tokens (or, by weight, the given share) are kept, bit by bit.
+  auto bisect = [&](bool by_weight, u64 want, double share) {
     u64 t = 0;
+    double target = 0.0;
+    if (by_weight) {
+      u64 v = 0;
+      each([&](float x, int i) {
+        if (keeps(x, i)) v += sample_weight(x, r);
+      });
+      target = share * static_cast<double>(cluster_all(sample_block_sum<THREADS>(v, s)));
+    }
     for (int bit = 63; bit >= 0; --bit) {
       const u64 c = t | (1ull << bit);
       u64 v = 0;
@@ -360,6 +384,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
     }
     return t;
   };
+  // A warp has a contiguous part [j0, j1) of the CTA's tokens.
+  const int per = (((n + WARPS - 1) / WARPS) + 127) & ~127;
+  const int j0 = min(n, warp * per), j1 = min(n, j0 + per);
+  // After a cut to p: weight of the warp's drawable tokens in bins before lo (behind hi none is left).
+  u64 base = 0;
+  int lo = 0, hi = kSampleBins;
   auto set_threshold = [&](u64 rank) {
     cx = sample_unkey(static_cast<uint32_t>(rank >> 32));    // always within the tokens kept so far
     ci = static_cast<int>(0xffffffffu - static_cast<uint32_t>(rank));
@@ -371,7 +401,6 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
   // what is left to do.
   enum { NOTHING, DRAW, CUT_P, RETRY };
   auto cut = [&](int k, bool by_p, bool by_thread) -> int {
-    u64 sum = 0;
     if (k > 0 && by_thread) {
       if (most > -INFINITY) atomicAdd(hist + sample_bin(most, r), 1u);
       __syncthreads();
@@ -381,19 +410,16 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
       });
       __syncthreads();
     } else {
+      const float cf = static_cast<float>(r.c);
       each([&](float x, int i) {
         const int b = sample_bin(x, r);
-        const u64 w = sample_weight(x, r);
-        if (keeps(x, i)) {
-          sum += w;
-          const int sh = sample_shift(b, r);
-          const uint32_t m = static_cast<uint32_t>((w + ((1ull << sh) >> 1)) >> sh);
-          if (m) atomicAdd(hist + b, m);
-        }
+        // 2^(44 - y - shift), at most 2^15 but for a rounding: 49152 of them fit 32 bits
+        const uint32_t m = __float2uint_rn(ex2_approx(static_cast<float>(44 - sample_shift(b, r)) - (r.mxf - x) * cf));
+        if (keeps(x, i) && m) atomicAdd(hist + b, m);
       });
-      sum = sample_block_sum<THREADS>(sum, s);
+      __syncthreads();
     }
-    const u64 total = cluster_all(sum);
+    cluster_sync_all();
     if (cr == 0) {
       // BPT bins per thread over the cluster: what lies before each, in tokens or in weight
       u64 v[BPT], sum = 0, all;
@@ -414,7 +440,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
       if (tid == 0) {
         s.cmd.lo = s.cmd.hi = k > 0 ? kSampleBins - 1 : 0;
         s.cmd.skip = k > 0 && !by_thread && static_cast<u64>(k) >= all;
-        s.cmd.total = total;
+        s.cmd.total = 0;
       }
       __syncthreads();
       // the bin in which the running value reaches the target (rounded weights: of their own total)
@@ -446,21 +472,42 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
                   "one 64-bit store");
     int result = SAMPLE_CUT;
     do {
-      u64 above = 0;                             // weight above the list
-      if (!cmd.skip)
+      u64 above = 0, all = 0;                    // weight above the list, and of all tokens
+      auto enlist = [&](float x, int i) {
+        const uint32_t at = atomic_add_cluster_u32(remote(&s.listed, 0), 1u);
+        if (at < kSampleList) st_cluster_u64(remote(list + at, 0), sample_rank(x, i));
+      };
+      if (k > 0 && !cmd.skip) {
         each([&](float x, int i) {
           if (!keeps(x, i)) return;
           const int b = sample_bin(x, r);
-          if (b >= cmd.lo && b <= cmd.hi) {
-            const uint32_t at = atomic_add_cluster_u32(remote(&s.listed, 0), 1u);
-            if (at < kSampleList) st_cluster_u64(remote(list + at, 0), sample_rank(x, i));
-          } else if (k == 0 && b < cmd.lo) {
-            above += sample_weight(x, r);
-          }
+          if (b >= cmd.lo && b <= cmd.hi) enlist(x, i);
         });
+      } else if (k == 0) {
+        base = 0;
+        for (int j = j0 + 4 * lane; j < j1; j += 128) {
+          float x[4];
+          sample_get4(xs, j >> 2, x);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int b = sample_bin(x[q], r);
+            const u64 w = keeps(x[q], i0 + j + q) ? sample_weight(x[q], r) : 0;
+            const u64 wa = b < cmd.lo ? w : 0;
+            all += w;
+            above += wa;
+            base += survives(wa) ? wa : 0;
+            if (b == cmd.lo && w) enlist(x[q], i0 + j + q);
+          }
+        }
+        base = sample_warp_reduce(base, [](u64 x, u64 y) { return x + y; });
+        lo = cmd.lo;
+        hi = cmd.hi;
+        above = sample_block_sum<THREADS>(above, s);
+        all = sample_block_sum<THREADS>(all, s);
+      }
       if (cr > 0)                                // for another cut
         for (int j = tid; j < kSampleBins; j += THREADS) hist[j] = 0;
-      above = cluster_all(k == 0 ? sample_block_sum<THREADS>(above, s) : 0);
+      all = cluster_all2(all, above);
       if (cmd.skip) {
         if (cr == 0)
           for (int j = tid; j < kSampleBins; j += THREADS) hist[j] = 0;
@@ -516,12 +563,15 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
           for (int size = 2; size <= m; size <<= 1)
             for (int d = size >> 1; d > 0; d >>= 1) {
               for (int j = tid; j < m / 2; j += THREADS) {
-                const int lo = 2 * j - (j & (d - 1)), hi = lo + d;
-                const u64 x = list[lo], y = list[hi];
-                if ((x < y) == ((lo & size) == 0)) list[lo] = y, list[hi] = x;
+                const int a = 2 * j - (j & (d - 1)), b = a + d;
+                const u64 x = list[a], y = list[b];
+                if ((x < y) == ((a & size) == 0)) list[a] = y, list[b] = x;
               }
-              __syncthreads();
+              // a distance up to 32 stays within the 64 entries of a warp, in this step and the next
+              if (d > 32 || (d == 1 && size >= 64)) __syncthreads();
+              else __syncwarp();
             }
+          __syncthreads();
           const int kk = k > 0 ? k - static_cast<int>(cmd.total) : len;   // entries that may stay
           int last = kk - 1;                     // the last kept one
           int found = SAMPLE_CUT;
@@ -534,7 +584,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
               sum += w[j];
             }
             u64 before = sample_block_scan<THREADS>(sum, tot, s) + above;
-            const double target = p * static_cast<double>(k == 0 ? cmd.total : tot);
+            const double target = p * static_cast<double>(k == 0 ? all : tot);
             u64 kept = 0;
 #pragma unroll
             for (int j = 0; j < BPT; ++j) {
@@ -563,27 +613,25 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
     if (result == SAMPLE_DRAWN) return NOTHING;
     if (result == SAMPLE_SHORT) {
       if (k > 0 && by_thread) return RETRY;
-      set_threshold(k > 0 ? bisect(false, static_cast<u64>(k), 0.0)
-                          : bisect(true, 0, p * static_cast<double>(cmd.total)));
+      set_threshold(bisect(k == 0, static_cast<u64>(k), p));
+      base = 0, lo = 0, hi = kSampleBins;
       return after;
     }
     set_threshold(s.cmd.C);
     return whole ? DRAW : after;
   };
   const bool by_p = p < 1.0;
-  int left = by_p ? CUT_P : DRAW;
-  if (top_k > 0 && top_k < a.V) {
-    // threads with a finite logit in the cluster: more than k of them, or count tokens
-    const u64 have = cluster_all(static_cast<u64>(__syncthreads_count(most > -INFINITY)));
-    left = have > static_cast<u64>(top_k) ? cut(top_k, by_p, true) : RETRY;
-    if (left == RETRY) left = cut(top_k, by_p, false);
+  int left = DRAW, k = top_k > 0 && top_k < a.V ? top_k : 0;
+  bool by_thread = k > 0 && have > static_cast<u64>(k);
+  for (bool more = k > 0 || by_p; more;) {     // one call: the cut stays inline, its state in registers
+    left = cut(k, by_p, by_thread);
+    more = left == RETRY || left == CUT_P;
+    if (left == CUT_P) k = 0;
+    by_thread = false;
   }
-  if (left == CUT_P) left = cut(0, true, false);
   if (left == NOTHING) return;
 
-  // ------------------------------------------------ the draw, in vocabulary order: a warp has a contiguous part
-  const int per = (((n + WARPS - 1) / WARPS) + 127) & ~127;
-  const int j0 = min(n, warp * per), j1 = min(n, j0 + per);
+  // ------------------------------------------------ the draw, in vocabulary order
   auto kept = [&](float x, int j) -> u64 {
     const u64 w = sample_weight(x, r);
     return keeps(x, i0 + j) && survives(w) ? w : 0ull;
@@ -597,29 +645,53 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
         mine += (f(x[0], j) + f(x[1], j + 1)) + (f(x[2], j + 2) + f(x[3], j + 3));
     }
   };
-  if (r.q > 0 || cx > -INFINITY) part(kept);
+  if (hi < kSampleBins)                        // the tokens above the list are in `base`
+    part([&](float x, int j) {
+      u64 w = 0;
+      if (keeps(x, i0 + j) && sample_bin(x, r) >= lo) w = kept(x, j);
+      return w;
+    });
+  else if (r.q > 0 || cx > -INFINITY) part(kept);
   else part([&](float x, int) { return sample_weight(x, r); });
-  mine = sample_warp_reduce(mine, [](u64 x, u64 y) { return x + y; });
-  __syncthreads();
-  if (lane == 0) s.red[warp] = mine;
-  __syncthreads();
-  u64 before = 0, block = 0;
+  mine = sample_warp_reduce(mine, [](u64 x, u64 y) { return x + y; }) + base;
+  // the sums of the warps before: of this CTA, then of the cluster
+  auto warps = [&](u64 v, u64& block) {
+    __syncthreads();
+    if (lane == 0) s.red[warp] = v;
+    __syncthreads();
+    u64 before = 0;
+    block = 0;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    if (w < warp) before += s.red[w];
-    block += s.red[w];
-  }
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) before += s.red[w];
+      block += s.red[w];
+    }
+    return before;
+  };
+  u64 block, before = warps(mine, block);
   if (tid < cs) st_cluster_u64(remote(&s.part[turn][cr], tid), block);
   cluster_sync_all();                          // the last access to another CTA's memory
-  u64 total = 0;
+  u64 total = 0, first = 0;
   for (int q = 0; q < cs; ++q) {
-    if (q < cr) before += s.part[turn][q];
+    if (q < cr) first += s.part[turn][q];
     total += s.part[turn][q];
   }
   const u64 target = goal(total);
-  if (before <= target && target < before + mine) {
-    for (int jb = j0; jb < j1; jb += 32) {
-      const u64 w = jb + lane < j1 ? kept(static_cast<float>(xs[jb + lane]), jb + lane) : 0;
+  if (target < first || target >= first + block) return;   // in another CTA's part
+  before += first;
+  if (before <= target && target < before + mine && lane == 0) s.listed = j0, s.red[0] = before;
+  __syncthreads();
+  // the part of the warp that has it, once more by all warps, then by the one that has it
+  const int g0 = s.listed, sub = per / WARPS < 32 ? 32 : (per / WARPS + 31) & ~31;
+  const u64 start = s.red[0];
+  const int k0 = min(n, g0 + warp * sub), k1 = min(min(n, g0 + per), k0 + sub);
+  u64 v = 0;
+  for (int j = k0 + lane; j < k1; j += 32) v += kept(static_cast<float>(xs[j]), j);
+  v = sample_warp_reduce(v, [](u64 x, u64 y) { return x + y; });
+  before = start + warps(v, block);
+  if (before <= target && target < before + v) {
+    for (int jb = k0; jb < k1; jb += 32) {
+      const u64 w = jb + lane < k1 ? kept(static_cast<float>(xs[jb + lane]), jb + lane) : 0;
       u64 incl = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
