@@ -13,6 +13,7 @@ Weights use the math orientation W[k, n] (Y = X W) unless ``transposed=True``.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -403,35 +404,26 @@ def row_parallel_forward_noalloc(X: torch.Tensor, packed_v: torch.Tensor, n: int
 
 
 # ---------------------------------------------------------------- serving: windows, caches, sampling
-# These calls run many times per second on little work, so their checks cost as little as
-# they can: one pass per tensor, and no device or stream switch where none is needed.
-class _On:
-    """The call's device and stream: makes the tensors' device current for the call and
-    allocates outputs on the stream that writes them. Yields the raw stream."""
+# These calls run many times per second on little work, so their host side costs as little
+# as it can: one check per tensor, the raw stream (torch.cuda.current_stream() alone takes
+# 3 us), and a device or stream switch only where the call needs one.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    __slots__ = ("dev", "stream", "guard", "on")
 
-    def __init__(self, dev: int, stream):
-        self.dev, self.stream, self.guard, self.on = dev, stream, None, None
+def _here(dev: int, stream) -> bool:
+    """Whether the call can run as it is: no stream given, and the tensors' device current."""
+    return stream is None and torch.cuda.current_device() == dev
 
-    def __enter__(self):
-        if self.stream is None and torch.cuda.current_device() == self.dev:
-            return torch.cuda.current_stream().cuda_stream
-        if self.stream is not None and self.stream.device.index != self.dev:
-            raise ValueError(f"stream of {self.stream.device}, tensors on cuda:{self.dev}")
-        self.guard = torch.cuda.device(self.dev)
-        self.guard.__enter__()
-        if self.stream is None:
-            return torch.cuda.current_stream().cuda_stream
-        self.on = torch.cuda.stream(self.stream)
-        self.on.__enter__()
-        return self.stream.cuda_stream
 
-    def __exit__(self, *exc):
-        if self.on is not None:
-            self.on.__exit__(*exc)
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+@contextlib.contextmanager
+def _there(dev: int, stream):
+    """The tensors' device, and the given stream of it, made current: outputs are then
+    allocated on the stream that writes them."""
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream of {stream.device}, tensors on cuda:{dev}")
+    with torch.cuda.device(dev):
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            yield
 
 
 def _arg(t, what: str, dtype, shape, dev: int | None) -> int | None:
@@ -441,7 +433,8 @@ def _arg(t, what: str, dtype, shape, dev: int | None) -> int | None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch.Tensor")
-    if not t.is_cuda:
+    on = t.get_device()
+    if on < 0 or not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
@@ -449,8 +442,8 @@ def _arg(t, what: str, dtype, shape, dev: int | None) -> int | None:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    if dev is not None and t.get_device() != dev:
-        raise ValueError(f"{what} is on cuda:{t.get_device()}, other arguments on cuda:{dev}")
+    if dev is not None and on != dev:
+        raise ValueError(f"{what} is on cuda:{on}, other arguments on cuda:{dev}")
     return t.data_ptr()
 
 
@@ -486,12 +479,14 @@ def sharded_window_attention(qkv: torch.Tensor, nseq: int, seqlen: int, heads: H
     pq = _arg(_need(qkv, "qkv"), "qkv", torch.bfloat16, (m, cols), None)
     dev = qkv.get_device()
     po = _arg(out, "out", torch.bfloat16, (m, ocols), dev)
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty(m, ocols, dtype=torch.bfloat16, device=qkv.device)
-            po = out.data_ptr()
-        _check(lib.sharded_window_attention(pq, nseq, seqlen, ctypes.byref(hd), tp, window, nsink, po, st),
-               "sharded_window_attention")
+    if not _here(dev, stream):
+        with _there(dev, stream):
+            return sharded_window_attention(qkv, nseq, seqlen, heads, tp, window, nsink, out)
+    if out is None:
+        out = torch.empty(m, ocols, dtype=torch.bfloat16, device=qkv.device)
+        po = out.data_ptr()
+    _check(lib.sharded_window_attention(pq, nseq, seqlen, ctypes.byref(hd), tp, window, nsink, po, _raw_stream(dev)),
+           "sharded_window_attention")
     return out
 
 
@@ -505,9 +500,11 @@ def sharded_kv_append(qkv: torch.Tensor, nseq: int, seqlen: int, heads: Heads, t
     pk, pv, cap = _cache_args(k_cache, v_cache, nseq, nkv, heads.head_dim, dev)
     pp = _arg(pos, "pos", torch.int32, (nseq,), dev)
     pc = _arg(count, "count", torch.int32, (nseq,), dev)
-    with _On(dev, stream) as st:
-        _check(lib.sharded_kv_append(pq, nseq, seqlen, ctypes.byref(hd), tp, pp, pc, nsink, pk, pv, cap, st),
-               "sharded_kv_append")
+    if not _here(dev, stream):
+        with _there(dev, stream):
+            return sharded_kv_append(qkv, nseq, seqlen, heads, tp, k_cache, v_cache, pos, count, nsink)
+    _check(lib.sharded_kv_append(pq, nseq, seqlen, ctypes.byref(hd), tp, pp, pc, nsink, pk, pv, cap,
+                                 _raw_stream(dev)), "sharded_kv_append")
 
 
 def tps_decode_workspace_bytes(nseq: int, heads: Heads, tp: int, prefix_len: int = 0) -> int:
@@ -538,12 +535,14 @@ def sharded_window_decode(qkv: torch.Tensor, heads: Heads, tp: int, pos: torch.T
     pp = _arg(_need(pos, "pos"), "pos", torch.int32, (nseq,), dev)
     pw = _arg(_need(ws, "ws"), "ws", None, None, dev)
     po = _arg(out, "out", torch.bfloat16, (nseq, ocols), dev)
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty(nseq, ocols, dtype=torch.bfloat16, device=qkv.device)
-            po = out.data_ptr()
-        _check(lib.sharded_window_decode(pq, nseq, ctypes.byref(hd), tp, pp, window, nsink, pk, pv, cap, po, pw,
-                                         ws.nbytes, st), "sharded_window_decode")
+    if not _here(dev, stream):
+        with _there(dev, stream):
+            return sharded_window_decode(qkv, heads, tp, pos, window, k_cache, v_cache, ws, nsink, out)
+    if out is None:
+        out = torch.empty(nseq, ocols, dtype=torch.bfloat16, device=qkv.device)
+        po = out.data_ptr()
+    _check(lib.sharded_window_decode(pq, nseq, ctypes.byref(hd), tp, pp, window, nsink, pk, pv, cap, po, pw,
+                                     ws.nbytes, _raw_stream(dev)), "sharded_window_decode")
     return out
 
 
@@ -566,12 +565,14 @@ def sharded_prefix_decode(qkv: torch.Tensor, heads: Heads, tp: int, prefix_k, pr
     pp = _arg(_need(pos, "pos"), "pos", torch.int32, (nseq,), dev)
     pw = _arg(_need(ws, "ws"), "ws", None, None, dev)
     po = _arg(out, "out", torch.bfloat16, (nseq, ocols), dev)
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty(nseq, ocols, dtype=torch.bfloat16, device=qkv.device)
-            po = out.data_ptr()
-        _check(lib.sharded_prefix_decode(pq, nseq, ctypes.byref(hd), tp, fk, fv, P, pp, pk, pv, cap, po, pw,
-                                         ws.nbytes, st), "sharded_prefix_decode")
+    if not _here(dev, stream):
+        with _there(dev, stream):
+            return sharded_prefix_decode(qkv, heads, tp, prefix_k, prefix_v, pos, k_cache, v_cache, ws, out)
+    if out is None:
+        out = torch.empty(nseq, ocols, dtype=torch.bfloat16, device=qkv.device)
+        po = out.data_ptr()
+    _check(lib.sharded_prefix_decode(pq, nseq, ctypes.byref(hd), tp, fk, fv, P, pp, pk, pv, cap, po, pw,
+                                     ws.nbytes, _raw_stream(dev)), "sharded_prefix_decode")
     return out
 
 
@@ -605,9 +606,11 @@ def logits_sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k
     m, V = logits.shape
     dev = logits.get_device()
     par = _sample_args(m, dev, u, temperature, top_k, top_p, min_p, out_idx, out_logp)
-    with _On(dev, stream) as st:
-        out_idx, out_logp = _sample_outputs(m, logits.device, par, out_idx, out_logp)
-        _check(lib.logits_sample(pl, _ydtype(logits.dtype), m, V, *par, st), "logits_sample")
+    if not _here(dev, stream):
+        with _there(dev, stream):
+            return logits_sample(logits, u, temperature, top_k, top_p, min_p, out_idx, out_logp)
+    out_idx, out_logp = _sample_outputs(m, logits.device, par, out_idx, out_logp)
+    _check(lib.logits_sample(pl, _ydtype(logits.dtype), m, V, *par, _raw_stream(dev)), "logits_sample")
     return out_idx, out_logp
 
 
@@ -624,10 +627,13 @@ def vocab_parallel_sample(X: torch.Tensor, H: int, V: int, tp: int, packed_w: to
         raise ValueError("packed_w is smaller than the COLUMN pack of W[H, V]")
     _arg(ws, "ws", None, None, dev)
     par = _sample_args(m, dev, u, temperature, top_k, top_p, min_p, out_idx, out_logp)
-    with _On(dev, stream) as st:
-        if ws is None:
-            ws = workspace(FN_SAMPLE, m, V, H, tp, device=X.device)
-        out_idx, out_logp = _sample_outputs(m, X.device, par, out_idx, out_logp)
-        _check(lib.vocab_parallel_sample(px, m, H, pw, V, tp, *par, ws.data_ptr(), ws.nbytes, st),
-               "vocab_parallel_sample")
+    if not _here(dev, stream):
+        with _there(dev, stream):
+            return vocab_parallel_sample(X, H, V, tp, packed_w, u, ws, temperature, top_k, top_p, min_p, out_idx,
+                                         out_logp)
+    if ws is None:
+        ws = workspace(FN_SAMPLE, m, V, H, tp, device=X.device)
+    out_idx, out_logp = _sample_outputs(m, X.device, par, out_idx, out_logp)
+    _check(lib.vocab_parallel_sample(px, m, H, pw, V, tp, *par, ws.data_ptr(), ws.nbytes, _raw_stream(dev)),
+           "vocab_parallel_sample")
     return out_idx, out_logp

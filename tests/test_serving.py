@@ -549,3 +549,30 @@ def test_refused_calls(T):
         T.logits_sample(z(2, 16, dtype=torch.float16), z(2, dtype=torch.float32))
     assert T.logits_sample(z(0, 16), z(0, dtype=torch.float32))[0].numel() == 0
     assert T.sharded_window_attention(z(0, cols), 0, 5, h, 2, 4).numel() == 0
+
+
+def test_explicit_stream(T):
+    """Every call on a stream given as an argument, behind work of that stream."""
+    st = torch.cuda.Stream()
+    h = T.Heads(4, 2, D)
+    nkv, cols = geom(4, 2, 2)
+    S, cap = 140, 150
+    qkv = WL.gen_normal((S, cols), 1.0, 995)
+    src, x = qkv.pin_memory(), torch.zeros(S, cols, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.zeros(1, nkv, cap, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws, pos = T.decode_workspace(1, h, 2), torch.tensor([S - 1], dtype=torch.int32, device="cuda")
+    logits, u, g = rows(3, 504, 2.0, 996)
+    lg, ug = logits.cuda(), u.cuda()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(2_000_000)
+        x.copy_(src, non_blocking=True)
+    A = T.sharded_window_attention(x, 1, S, h, 2, 60, 3, stream=st)
+    T.sharded_kv_append(x[:S - 1], 1, S - 1, h, 2, k, v, nsink=3, stream=st)
+    out = T.sharded_window_decode(x[S - 1:], h, 2, pos, 60, k, v, ws, nsink=3, stream=st)
+    idx, _ = T.logits_sample(lg, ug, stream=st)
+    st.synchronize()
+    ref, mag = O.window_attention_sharded(qkv, 4, 2, D, 2, 1, S, 60, 3)
+    close(A, ref, mag)
+    close(out, ref[-1:], mag[-1:])
+    assert np.array_equal(idx.cpu().numpy(), sample_ref(logits, u)[0])
