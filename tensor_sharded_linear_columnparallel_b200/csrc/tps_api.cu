@@ -1674,9 +1674,6 @@ int sharded_kv_append(const void* qkv, int64_t nseq, int64_t seqlen, const tps_h
   int rc = cache_geom(heads, tp, nsink, cap, &hm);
   if (rc) return rc;
   if (nseq > (1LL << 30) || seqlen > (1LL << 30) || nseq * seqlen > (1LL << 30)) return TPS_ERR_ARG;
-  // one block of 256 threads copies 16 rows of 256 bytes: the grid has to fit 31 bits
-  const int64_t nkv = static_cast<int64_t>(tp) * hm.kvs;
-  if (nseq * seqlen > (1LL << 34) / nkv) return TPS_ERR_ARG;
   if (nseq * seqlen == 0) return TPS_OK;
   if (qkv == nullptr || k_cache == nullptr || v_cache == nullptr) return TPS_ERR_ARG;
   if (!aligned16(qkv) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(pos) || !aligned4(count))

@@ -492,10 +492,10 @@ int launch_prefix_attention(const CUtensorMap& tq, const CUtensorMap& tk, const 
 }
 
 int launch_kv_append(const KvAppendArgs& a, cudaStream_t st) {
-  const long long units = static_cast<long long>(a.nseq) * a.S * a.tp * 2 * a.kvs * 16;
-  const long long grid = (units + kAppendThreads - 1) / kAppendThreads;
-  LaunchCfg lc(static_cast<int>(grid), 0, st, 1, kAppendThreads, true);
-  if (cudaLaunchKernelEx(&lc.cfg, tps_kv_append_kernel, a) != cudaSuccess) return -6;
+  // at most min(S, cap) tokens of a sequence keep a slot
+  const int groups = ((a.S < a.cap ? a.S : a.cap) + kAppendTokens - 1) / kAppendTokens;
+  LaunchCfg lc(a.nseq * groups, 0, st, 1, kAppendThreads, true);
+  if (cudaLaunchKernelEx(&lc.cfg, tps_kv_append_kernel, a, groups) != cudaSuccess) return -6;
   return cudaGetLastError() == cudaSuccess ? 0 : -6;
 }
 
