@@ -90,7 +90,8 @@ __global__ void __launch_bounds__(kAppendThreads) tps_kv_append_kernel(const KvA
 //    one vote per block, and a reduction over the block only then (always at an item's
 //    first block). The weights are rounded to bf16 for the product, as in the prefill; the
 //    sum keeps them in fp32, a partial sum per thread until the item ends.
-constexpr int kDecThreads = 7 * 32;
+constexpr int kDecWarps = 14;                                     // warps 7-13 only merge
+constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kDecStages = 3;
 constexpr int kDecHeads = 16;                                     // heads per item
 constexpr int kDecStageBytes = 2 * kAttnTileBytes;                // K and V of one block
@@ -269,13 +270,14 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
 }
 
 // Merges the n parts of one output row with one warp, a lane holding four dimensions.
-// part(c): the address of part c's 128 outputs, with its max and sum in m and l. The
-// loads of 20 parts are in flight before the first is used.
+// part(c): the address of part c's outputs, with its max and sum in m and l; the lane's
+// float4 is `lane` of the first `rows` parts (a row of 128 numbers) and `image` of the others.
+// The loads of 18 parts are in flight before the first is used.
 template <class Part>
-__device__ __forceinline__ void dec_merge(int n, int lane, Part part, __nv_bfloat16* dst) {
+__device__ __forceinline__ void dec_merge(int n, int rows, int lane, int image, Part part, __nv_bfloat16* dst) {
   float M = -INFINITY, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kIn = 20;
+  constexpr int kIn = 18;
   for (int c0 = 0; c0 < n; c0 += kIn) {
     const int k = min(kIn, n - c0);
     const float* o = nullptr;
@@ -286,7 +288,7 @@ __device__ __forceinline__ void dec_merge(int n, int lane, Part part, __nv_bfloa
     for (int i = 0; i < kIn; ++i) {
       const float4* p = reinterpret_cast<const float4*>(static_cast<uintptr_t>(
           __shfl_sync(0xffffffffu, static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(o)), i)));
-      v[i] = i < k ? __ldcg(p + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[i] = i < k ? __ldcg(p + (c0 + i < rows ? lane : image)) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     float mx = m;
 #pragma unroll
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   int* last_flag = reinterpret_cast<int*>(gbase + kDecOffBar + 172);    // [4]: cut items, their other CTAs
   DecWork* sWork = reinterpret_cast<DecWork*>(gbase + kDecOffBar + 192);
   static_assert(192 + sizeof(DecWork) <= 256, "barrier block");
-  int* scan = reinterpret_cast<int*>(gbase + kDecOffRed);   // [8] before the roles start
+  int* scan = reinterpret_cast<int*>(gbase + kDecOffRed);   // [kDecWarps] before the roles start
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -389,7 +391,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
     int total = 0, excl = incl - sum;
-    for (int i = 0; i < kDecThreads / 32; ++i) {
+    for (int i = 0; i < kDecWarps; ++i) {
       if (i < warp) excl += scan[i];
       total += scan[i];
     }
@@ -422,7 +424,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (lane == 31) scan[warp] = incl;
         __syncthreads();
         excl = before + incl - n;
-        for (int i = 0; i < kDecThreads / 32; ++i) {
+        for (int i = 0; i < kDecWarps; ++i) {
           if (i < warp) excl += scan[i];
           before += scan[i];
         }
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem_base, 64);
-  } else {
+  } else if (warp < 6) {
     // -------------------------------------------------- softmax and output (warps 2-5)
     // The four warps meet in named barriers, which cannot time out: a warp whose bounded
     // wait failed keeps coming to them and reports there, and all four leave together.
@@ -787,7 +789,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const int c0 = whole ? cta : dec_owner(w, it.s);
       const int nw = whole ? 1 : dec_owner(w, it.s + it.nb - 1) - c0 + 1;
       for (int h = 0; h < gc; ++h, ++job) {
-        if (job % (kDecThreads / 32) != warp) continue;
+        if (job % kDecWarps != warp) continue;
         auto part = [&](int c, float& m, float& l) -> const float* {
           if (c < nw) {
             const float* sl = dec_part(a, w, it, c0 + c);
@@ -801,9 +803,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           const int pr = (it.b % per) * G + h0 + h;
           m = __ldcg(a.prefix_ml + pt * 256 + pr);
           l = __ldcg(a.prefix_ml + pt * 256 + 128 + pr);
-          return a.prefix_parts + (pt * 128 + pr) * kAttnD;
+          return a.prefix_parts + pt * 128 * kAttnD;
         };
-        dec_merge(nw + (a.prefix_parts ? a.prefix_splits : 0), lane, part,
+        const int pr = a.prefix_parts ? (it.b % (128 / G)) * G + h0 + h : 0;
+        dec_merge(nw + (a.prefix_parts ? a.prefix_splits : 0), nw, lane, attn_part_index(pr, lane), part,
                   a.out + static_cast<long long>(it.b) * a.ldo +
                       static_cast<long long>(r * a.qs + lk * G + h0 + h) * kAttnD);
       }

@@ -102,8 +102,8 @@ struct AttnArgs {
   // PREFIX kernel: S is the prefix length; `grp` query heads per KV head slot; a tile is
   // the rows of bpt sequences (row = sequence * grp + head); the key blocks of a KV head
   // slot are cut into `splits` parts. Part p = (slot * tiles + tile) * splits + split:
-  // parts[p][128][128] (unnormalised output), ml[p][2][128] (reference max in log2 units,
-  // sum).
+  // parts[p][128 * 128] (unnormalised output, an image of attn_part_index), ml[p][2][128]
+  // (reference max in log2 units, sum).
   float *parts, *ml;
   int nkv, bpt, tiles, splits;
 };
