@@ -1236,7 +1236,9 @@ int run_decode(const void* qkv, int64_t nseq, const tps_heads* heads, const Head
   if (!aligned16(qkv) || !aligned4(pos) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(attn_out) ||
       !aligned16(ws))
     return TPS_ERR_ALIGN;
-  const int64_t blocks = nseq * nkv * ((hm.qs / hm.kvs + 15) / 16) * ((cap + 127) / 128);   // at most
+  // an item costs about one block besides its stream, two when it is merged with a prefix
+  const int room = prefix_len > 0 ? 2 : 1;
+  const int64_t blocks = nseq * nkv * ((hm.qs / hm.kvs + 15) / 16) * (room + (cap + 127) / 128 + 1);   // at most
   if (blocks > 0x7fffffffLL) return TPS_ERR_ARG;
   const int sms = num_sms_current();
   const DecodeWs lay = decode_ws(nseq, hm, nkv, prefix_len, sms);
@@ -1261,6 +1263,7 @@ int run_decode(const void* qkv, int64_t nseq, const tps_heads* heads, const Head
   a->out = static_cast<__nv_bfloat16*>(attn_out);
   a->ldo = heads->hq * d;
   a->nch = lay.nch;
+  a->room = room;
   a->counters = reinterpret_cast<int*>(wsp + lay.counters);
   a->parts = reinterpret_cast<float*>(wsp + lay.parts);
   a->timeout_ns = kTimeoutNs;

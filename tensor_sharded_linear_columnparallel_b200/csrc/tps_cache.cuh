@@ -68,8 +68,9 @@ __global__ void __launch_bounds__(kAppendThreads) tps_kv_append_kernel(const KvA
 // ---------------------------------------------------------------- decode
 // One new token per sequence, G = qs / kvs query heads per KV head slot. The work is the
 // stream of the visible keys (512 bytes each), so it is cut by bytes: the 128-slot blocks
-// of all (sequence, KV head slot, chunk of 16 heads) items are numbered in one line and
-// every CTA (one per SM) takes an equal part of it, wherever that begins and ends. An item
+// of all (sequence, KV head slot, chunk of 16 heads) items stand in one line, each item
+// with some blocks' room ahead of it for what it costs besides its stream, and every CTA
+// (one per SM) takes an equal part of the line, wherever that begins and ends. An item
 // cut by a border leaves its parts (running max, sum, unnormalised output, fp32) in the
 // workspace, and the CTA that finishes last merges them; its counter returns to zero.
 // Behind a shared prefix every item leaves a part, to be merged with the prefix kernel's.
@@ -148,66 +149,73 @@ __device__ __forceinline__ bool dec_sees(const DecodeArgs& a, const DecView& v, 
   return slot < a.cap && age < v.ring;
 }
 
-// The line of blocks of all items (sequence, then KV head slot, then chunk), and the part
-// [w0, w1) of it that this CTA works on: the first `rem` CTAs take share + 1 blocks, the
-// others share. It has fewer than 2^31 blocks (the host checks: 2^31 blocks are 128 TB).
+// The line of all items (sequence, then KV head slot, then chunk): an item of nb blocks
+// has a.room + nb places, block i at place room + i of them. This CTA works on the places
+// [w0, w1): the first `rem` CTAs take share + 1, the others share. The line has fewer than
+// 2^31 places (the host checks).
+// The room is what an item costs besides its stream, in blocks (1.4 us): with none, 64
+// sequences of 1 to 512 tokens behind a prefix left CTAs with nine items of one block each
+// that took 27 us for their part of the line, those with three of three blocks 19.
 struct DecWork {
-  int ctas, share, rem;        // CTAs with work (at most the grid, at most one per block)
+  int ctas, share, rem;        // CTAs with work (at most the grid, at most one per place)
   int w0, w1;
   int b, t;                    // the sequence that w0 lies in, its token's position
-  int base;                    // line index of that sequence's first block
+  int base;                    // place where that sequence's first item begins
 };
 
 __device__ __forceinline__ int dec_border(const DecWork& w, int cta) { return cta * w.share + min(cta, w.rem); }
-// The CTA that works on block x of the line.
+// The CTA that works on place x of the line.
 __device__ __forceinline__ int dec_owner(const DecWork& w, int x) {
   const int head = w.rem * (w.share + 1);
   return x < head ? x / (w.share + 1) : w.rem + (x - head) / w.share;
+}
+__device__ __forceinline__ int dec_places(const DecodeArgs& a, const DecView& v) {   // of one item
+  const int nb = v.blocks();
+  return nb ? a.room + nb : 0;
 }
 
 // One item as a CTA meets it: blocks [i0, i1) of its nb are this CTA's.
 struct DecItem {
   int b, g, ch;                // sequence, KV head slot, chunk of 16 heads
   int nb, i0, i1;
-  int s;                       // line index of its first block
+  int s;                       // place of its first block
   DecView v;
   __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == nb; }
 };
 
 // Walks the items of a CTA's part in order; every role walks them by itself.
 struct DecWalk {
-  int x, b, k, tnext;          // next block; its sequence; item within the sequence; position of sequence b + 1
+  int b, k, tnext;             // next item: its sequence, its number there; position of sequence b + 1
+  int at;                      // where it begins
   DecView v;
-  __device__ __forceinline__ DecWalk(const DecodeArgs& a, const DecWork& w) : x(w.w0), b(w.b), k(0) {
+  __device__ __forceinline__ DecWalk(const DecodeArgs& a, const DecWork& w) : b(w.b), k(0) {
     v = dec_view(a, w.t);
     tnext = b + 1 < a.nseq ? __ldcg(a.pos + b + 1) : -1;
-    if (w.w0 < w.w1) k = (w.w0 - w.base) / v.blocks();
-    s = w.base + k * v.blocks();
+    if (w.w0 < w.w1) k = (w.w0 - w.base) / dec_places(a, v);
+    at = w.base + k * dec_places(a, v);
   }
   __device__ __forceinline__ bool next(const DecodeArgs& a, const DecWork& w, DecItem& it) {
-    if (x >= w.w1) return false;
-    while (k == a.nkv * a.nch || v.blocks() == 0) {             // the next sequence with blocks
-      v = dec_view(a, tnext);
-      ++b;
-      tnext = b + 1 < a.nseq ? __ldcg(a.pos + b + 1) : -1;
-      k = 0;
-    }
-    it.b = b;
-    it.g = a.nch == 1 ? k : k / a.nch;
-    it.ch = k - it.g * a.nch;
-    it.nb = v.blocks();
-    it.s = s;
-    it.i0 = x - s;
-    it.i1 = min(it.nb, w.w1 - s);
-    it.v = v;
-    s += it.nb;
-    x = it.s + it.i1;
-    ++k;
+    do {
+      if (at >= w.w1 || w.w0 == w.w1) return false;
+      while (k == a.nkv * a.nch || v.blocks() == 0) {           // the next sequence with blocks
+        v = dec_view(a, tnext);
+        ++b;
+        tnext = b + 1 < a.nseq ? __ldcg(a.pos + b + 1) : -1;
+        k = 0;
+      }
+      it.b = b;
+      it.g = a.nch == 1 ? k : k / a.nch;
+      it.ch = k - it.g * a.nch;
+      it.nb = v.blocks();
+      it.s = at + a.room;
+      it.i0 = max(0, w.w0 - it.s);
+      it.i1 = min(it.nb, w.w1 - it.s);
+      it.v = v;
+      at = it.s + it.nb;
+      ++k;
+    } while (it.i0 >= it.i1);                                   // only its room is this CTA's
     return true;
   }
-
- private:
-  int s;                       // line index of item k
 };
 
 // Where CTA cta leaves its part of an item: per item where it has the whole of it (behind a
@@ -379,10 +387,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   {
     const int per = a.nkv * a.nch;
     const int t0 = threadIdx.x < a.nseq ? __ldcg(a.pos + threadIdx.x) : -1;
-    const int n0 = per * dec_view(a, t0).blocks();
+    const int n0 = per * dec_places(a, dec_view(a, t0));
     int sum = n0;
     for (int b = threadIdx.x + kDecThreads; b < a.nseq; b += kDecThreads)
-      sum += per * dec_view(a, __ldcg(a.pos + b)).blocks();
+      sum += per * dec_places(a, dec_view(a, __ldcg(a.pos + b)));
     int incl = sum;                         // with one sequence per thread, also the scan below
     for (int x = 1; x < 32; x <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, incl, x);
@@ -414,7 +422,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       if (a.nseq > kDecThreads) {
         if (b0 > 0) {
           t = b < a.nseq ? __ldcg(a.pos + b) : -1;
-          n = per * dec_view(a, t).blocks();
+          n = per * dec_places(a, dec_view(a, t));
         }
         incl = n;
         for (int x = 1; x < 32; x <<= 1) {
@@ -452,6 +460,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       // ------------------------------------------------ K and V of every block
       long long n = 0;
       bool ok = true;
+      // read once in a call: the parts, which are read back, stay in L2 instead
+      const uint64_t policy = l2_policy_evict_first();
       DecWalk walk(a, w);
       DecItem it;
       while (ok && walk.next(a, w, it)) {
@@ -465,10 +475,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           const uint32_t dst = base + st * kDecStageBytes;
           const int slot0 = it.v.block(i) * kAttnBlk;
           mbar_arrive_expect_tx(kv_full(st), kDecStageBytes);
-          tma_load_3d(dst, &tmK, kv_full(st), 0, slot0, row);
-          tma_load_3d(dst + kAttnHalf, &tmK, kv_full(st), 64, slot0, row);
-          tma_load_3d(dst + kAttnTileBytes, &tmV, kv_full(st), 0, slot0, row);
-          tma_load_3d(dst + kAttnTileBytes + kAttnHalf, &tmV, kv_full(st), 64, slot0, row);
+          tma_load_3d_hint(dst, &tmK, kv_full(st), 0, slot0, row, policy);
+          tma_load_3d_hint(dst + kAttnHalf, &tmK, kv_full(st), 64, slot0, row, policy);
+          tma_load_3d_hint(dst + kAttnTileBytes, &tmV, kv_full(st), 0, slot0, row, policy);
+          tma_load_3d_hint(dst + kAttnTileBytes + kAttnHalf, &tmV, kv_full(st), 64, slot0, row, policy);
         }
       }
       // wait (bounded) for the copies still in flight before the CTA may exit
@@ -522,7 +532,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     bool ok = true, any = false;
     DecWalk walk(a, w);
     DecItem it;
-    // the block is loaded: new rows in, unseen V rows out, then S^T = K Q^T
+    // the block is loaded: the new K row in and S^T = K Q^T issued, then, while that runs, the
+    // new V row in and the unseen V rows out
     auto issue_s = [&](int i, long long nn) -> bool {
       const int st = static_cast<int>(nn % kDecStages);
       if (!__all_sync(0xffffffffu, mbar_wait(kv_full(st), static_cast<uint32_t>((nn / kDecStages) & 1), abort_flag,
@@ -530,7 +541,28 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         return false;
       const uint32_t kb = base + st * kDecStageBytes, vb = kb + kAttnTileBytes;
       const int slot0 = it.v.block(i) * kAttnBlk;
-      bool touched = false;
+      const int nr = it.v.slot - slot0;
+      const bool fresh = nr >= 0 && nr < kAttnBlk;
+      const uint4 x = ld_shared_v4(base + kDecOffNew + (q & 1) * 512 + lane * 16);
+      if (fresh) {
+        if (lane < 16) st_shared_v4(kb + sw128_chunk(nr, lane, kAttnHalf), x.x, x.y, x.z, x.w);
+        fence_proxy_async_shared();
+      }
+      __syncwarp();
+      if (lane == 0) {
+        tc_fence_after();
+        const uint32_t sq = base + kDecOffQ + (q & 1) * kDecOpBytes;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint64_t off = static_cast<uint64_t>((kk & 3) * 2);   // 16 dimensions = 32 B along K
+          umma_bf16(tmem_base + static_cast<uint32_t>(nn & 1) * kDecHeads,
+                    smem_desc_sw128(kb + (kk < 4 ? 0 : kAttnHalf)) + off,
+                    smem_desc_sw128(sq + (kk < 4 ? 0 : kDecOpBytes / 2)) + off, kDecIdescS, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(s_full(static_cast<int>(nn & 1)));
+      }
+      __syncwarp();
+      bool touched = fresh;
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
         const int row = 32 * k + lane;
@@ -544,27 +576,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         touched |= __any_sync(0xffffffffu, !see);
       }
-      const int nr = it.v.slot - slot0;
-      if (nr >= 0 && nr < kAttnBlk) {
-        const uint4 x = ld_shared_v4(base + kDecOffNew + (q & 1) * 512 + lane * 16);
-        st_shared_v4((lane < 16 ? kb : vb) + sw128_chunk(nr, lane & 15, kAttnHalf), x.x, x.y, x.z, x.w);
-        touched = true;
-      }
+      if (fresh && lane >= 16) st_shared_v4(vb + sw128_chunk(nr, lane & 15, kAttnHalf), x.x, x.y, x.z, x.w);
       if (touched) fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) {
-        tc_fence_after();
-        const uint32_t sq = base + kDecOffQ + (q & 1) * kDecOpBytes;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint64_t off = static_cast<uint64_t>((kk & 3) * 2);   // 16 dimensions = 32 B along K
-          umma_bf16(tmem_base + static_cast<uint32_t>(nn & 1) * kDecHeads,
-                    smem_desc_sw128(kb + (kk < 4 ? 0 : kAttnHalf)) + off,
-                    smem_desc_sw128(sq + (kk < 4 ? 0 : kDecOpBytes / 2)) + off, kDecIdescS, kk > 0 ? 1u : 0u);
-        }
-        umma_commit(s_full(static_cast<int>(nn & 1)));
-        if (i == it.i1 - 1) umma_commit(q_empty(q & 1));
-      }
+      if (lane == 0 && i == it.i1 - 1) umma_commit(q_empty(q & 1));
       __syncwarp();
       return true;
     };
