@@ -1238,7 +1238,7 @@ int run_decode(const void* qkv, int64_t nseq, const tps_heads* heads, const Head
     return TPS_ERR_ALIGN;
   // an item costs about one block besides its stream, two when it is merged with a prefix
   const int room = prefix_len > 0 ? 2 : 1;
-  const int64_t blocks = nseq * nkv * ((hm.qs / hm.kvs + 15) / 16) * (room + (cap + 127) / 128 + 1);   // at most
+  const int64_t blocks = nseq * nkv * ((hm.qs / hm.kvs + 15) / 16) * (room + (cap + 127) / 128);   // places, at most
   if (blocks > 0x7fffffffLL) return TPS_ERR_ARG;
   const int sms = num_sms_current();
   const DecodeWs lay = decode_ws(nseq, hm, nkv, prefix_len, sms);
@@ -1274,6 +1274,7 @@ int run_decode(const void* qkv, int64_t nseq, const tps_heads* heads, const Head
   rc = make_map(&tk, k_cache, d, ucap, planes, row, row * ucap, 128, 1);
   if (rc == TPS_OK) rc = make_map(&tv, v_cache, d, ucap, planes, row, row * ucap, 128, 1);
   if (rc) return rc;
+  int64_t prefix_items = 0;
   if (prefix_len > 0) {
     tps::AttnArgs p{};
     p.nseq = a->nseq;
@@ -1291,9 +1292,9 @@ int run_decode(const void* qkv, int64_t nseq, const tps_heads* heads, const Head
     p.bpt = lay.bpt;
     p.tiles = lay.tiles;
     p.splits = lay.splits;
-    const int64_t items = nkv * ((lay.tiles + 1) / 2) * lay.splits;
-    if (items > (1LL << 30)) return TPS_ERR_ARG;
-    p.items = static_cast<int>(items);
+    prefix_items = nkv * ((lay.tiles + 1) / 2) * lay.splits;
+    if (prefix_items > (1LL << 30)) return TPS_ERR_ARG;
+    p.items = static_cast<int>(prefix_items);
     CUtensorMap tq, tpk, tpv;
     // a QKV row as heads of 128 columns: one box is the query heads of one KV head slot of bpt rows
     const uint64_t hrow = static_cast<uint64_t>(a->ld) / d, P = static_cast<uint64_t>(prefix_len);
@@ -1308,8 +1309,19 @@ int run_decode(const void* qkv, int64_t nseq, const tps_heads* heads, const Head
     a->prefix_tiles = lay.tiles;
     a->prefix_splits = lay.splits;
   }
-  return tps::launch_decode(tk, tv, *a, static_cast<int>(std::min<int64_t>(blocks, sms)), st) == 0 ? TPS_OK
-                                                                                                  : TPS_ERR_CUDA;
+  // Behind a prefix kernel that leaves SMs free, a short line is worked on there while it runs,
+  // where a CTA on every SM would have to wait for its own: by the longest times of the two
+  // (a place 1.4 us, a block of the prefix 2.2 us, 5 us to start and end either).
+  int grid = static_cast<int>(std::min<int64_t>(blocks, sms));
+  const int spare = prefix_len > 0 ? sms - static_cast<int>(std::min<int64_t>(prefix_items, sms)) : 0;
+  if (spare > 0) {
+    const double prefix_us = 5.0 + 2.2 * static_cast<double>((prefix_items + sms - 1) / sms) *
+                                       static_cast<double>((lay.nkb + lay.splits - 1) / lay.splits);
+    const double on_all = prefix_us + 5.0 + 1.4 * static_cast<double>(blocks) / sms;
+    const double on_spare = std::max(prefix_us, 5.0 + 1.4 * static_cast<double>(blocks) / spare);
+    if (on_spare < on_all) grid = std::min(grid, spare);
+  }
+  return tps::launch_decode(tk, tv, *a, grid, st) == 0 ? TPS_OK : TPS_ERR_CUDA;
 }
 
 }  // namespace

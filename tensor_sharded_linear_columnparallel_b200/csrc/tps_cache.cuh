@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kAppendThreads) tps_kv_append_kernel(const KvA
 //    one vote per block, and a reduction over the block only then (always at an item's
 //    first block). The weights are rounded to bf16 for the product, as in the prefill; the
 //    sum keeps them in fp32, a partial sum per thread until the item ends.
-constexpr int kDecWarps = 14;                                     // warps 7-13 only merge
+constexpr int kDecWarps = 12;                                     // warps 7-11 only merge; more would leave each 128 registers
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kDecStages = 3;
 constexpr int kDecHeads = 16;                                     // heads per item
