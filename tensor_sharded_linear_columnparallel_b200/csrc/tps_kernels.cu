@@ -486,9 +486,13 @@ int launch_window_attention(const CUtensorMap& tqkv, const AttnArgs& a, int grid
 
 int launch_prefix_attention(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a,
                             int grid, cudaStream_t st) {
+  // In clusters of two, so that its CTAs fill pairs of SMs: the decode kernel's CTAs that start
+  // beside it then have pairs of their own. Where they shared one, their stream held up the
+  // neighbour's loads until it ended (back to back, 64 sequences behind a prefix of 16384: 6 to
+  // 8 of 128 CTAs took 42 us instead of 25, the whole 87 us; so 75).
   static unsigned long long attr_done = 0ull;
-  return launch_with_smem(tps_attn2_kernel<ATTN_PREFIX>, &attr_done, kAttn2Threads, kAttn2SmemBytes, grid, st, 1,
-                          kAttn2SmemBytes, tq, tk, tv, a);
+  return launch_with_smem(tps_attn2_kernel<ATTN_PREFIX>, &attr_done, kAttn2Threads, kAttn2SmemBytes,
+                          (grid + 1) / 2 * 2, st, 2, kAttn2SmemBytes, tq, tk, tv, a);
 }
 
 int launch_kv_append(const KvAppendArgs& a, cudaStream_t st) {
