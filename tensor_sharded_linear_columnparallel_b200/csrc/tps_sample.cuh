@@ -238,6 +238,11 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
   const int top_k = a.top_k ? a.top_k[row] : 0;
   const double u = fmin(fmax(static_cast<double>(a.u[row]), 0.0), 1.0);    // NaN: 0
   const bool greedy = !(T >= 7.888609e-31f);   // 2^-100: the bins' scale stays finite
+  // what needs 64-bit arithmetic and not the row: ahead of the loads that it can wait for
+  SampleRow r;
+  r.c = 1.4426950408889634 / static_cast<double>(T);
+  r.q = qf > 0.0f ? static_cast<u64>(ceil(fmin(static_cast<double>(qf), 1.0) * static_cast<double>(kSampleOne))) : 0;
+  const float cf = static_cast<float>(r.c);
 
   // ------------------------------------------------ the row into shared memory, its largest and smallest logit
   float mx = -INFINITY, mn = INFINITY;         // neither takes a NaN
@@ -341,15 +346,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
     have = 0;                                  // top_k counts tokens
     __syncthreads();
   }
-  SampleRow r;
   r.mxf = mx;
   r.mx = static_cast<double>(mx);
-  r.c = 1.4426950408889634 / static_cast<double>(T);
-  r.q = qf > 0.0f ? static_cast<u64>(ceil(fmin(static_cast<double>(qf), 1.0) * static_cast<double>(kSampleOne))) : 0;
   // 2^octave bins per factor of 2 in the weight: as many as keep the range within the bins
-  const float span = fminf((mx - mn) * static_cast<float>(r.c), 46.2f);    // in factors of 2; 46.2 = 32 log2(e)
+  const float span = fminf((mx - mn) * cf, 46.2f);    // in factors of 2; 46.2 = 32 log2(e)
   const int octave = span > 0.0f ? min(100, ilogbf(static_cast<float>(kSampleBins - 1) / span)) : 0;   // at least 4
-  r.bin_scale = scalbnf(static_cast<float>(r.c), octave);
+  r.bin_scale = scalbnf(cf, octave);
   r.octave = min(octave, 31);
   const double p = static_cast<double>(pf);
   auto survives = [&](u64 w) { return w >= r.q; };         // min_p
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
   };
   auto draw = [&](int i, u64 w, u64 total) {
     a.out_idx[row] = i;
-    if (a.out_logp) a.out_logp[row] = static_cast<float>(log(static_cast<double>(w) / static_cast<double>(total)));
+    if (a.out_logp) a.out_logp[row] = logf(static_cast<float>(static_cast<double>(w) / static_cast<double>(total)));
   };
 
   // Largest threshold at which `want` tokens (or, by weight, the given share) are kept, bit by bit.
@@ -410,7 +412,6 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
       });
       __syncthreads();
     } else {
-      const float cf = static_cast<float>(r.c);
       each([&](float x, int i) {
         const int b = sample_bin(x, r);
         // 2^(44 - y - shift), at most 2^15 but for a rounding: 49152 of them fit 32 bits
@@ -530,8 +531,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
           __syncthreads();
           int place = 0;
           u64 larger = 0;
-          for (int j = half; j < len; j += TPE)
-            if (list[j] > re) ++place, larger += w[j];
+#pragma unroll 4
+          for (int j = half; j < len; j += TPE) {
+            const bool before = list[j] > re;
+            place += before;
+            larger += before ? w[j] : 0;
+          }
 #pragma unroll
           for (int o = 1; o < TPE; o <<= 1) {
             place += __shfl_xor_sync(0xffffffffu, place, o);
@@ -548,8 +553,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
           const u64 tot = sample_block_sum<THREADS>(in && half == 0 ? we : 0, s);
           const uint32_t ie = static_cast<uint32_t>(re);           // ~index: larger is earlier
           u64 upto = 0;
-          for (int j = half; j < len; j += TPE)
-            if (static_cast<uint32_t>(list[j]) >= ie) upto += w[j];
+#pragma unroll 4
+          for (int j = half; j < len; j += TPE) upto += static_cast<uint32_t>(list[j]) >= ie ? w[j] : 0;
 #pragma unroll
           for (int o = 1; o < TPE; o <<= 1) upto += __shfl_xor_sync(0xffffffffu, upto, o);
           const u64 t = goal(tot);
