@@ -414,8 +414,8 @@ TPS_API size_t tps_decode_workspace_bytes(int64_t nseq, const tps_heads* heads, 
  *              top_k <= 0 or >= V keeps all
  *     top_p    of what is left, in descending order (equal logits: the lower index
  *              first), keeps token j when the weight before it is below top_p times the
- *              sum, the first always; top_p >= 1 keeps all
- *     min_p    keeps w_i >= min_p, the largest always; min_p <= 0 keeps all
+ *              sum, the first always; top_p >= 1 (or NaN) keeps all
+ *     min_p    keeps w_i >= min_p, the largest always; min_p <= 0 (or NaN) keeps all
  *     draw     out_idx = the first kept index, in vocabulary order, whose running sum of
  *              kept weights exceeds u times their total
  *     out_logp = log of the drawn token's share of the kept weight

@@ -576,3 +576,114 @@ def test_explicit_stream(T):
     close(A, ref, mag)
     close(out, ref[-1:], mag[-1:])
     assert np.array_equal(idx.cpu().numpy(), sample_ref(logits, u)[0])
+
+
+# ============================================================ the ends of the ranges
+@pytest.mark.parametrize("prefix", [0, 200])
+def test_decode_more_sequences_than_threads(T, prefix):
+    """900 sequences, a third of them unused: the kernel's scan over the positions takes
+    several steps."""
+    hq, hkv, tp, cap, n = 4, 1, 1, 40, 900
+    nkv, cols = geom(hq, hkv, tp)
+    h = T.Heads(hq, hkv, D)
+    g = torch.Generator().manual_seed(7)
+    pos = torch.randint(-20, cap, (n,), generator=g, dtype=torch.int32)
+    qkv = WL.gen_normal((n, cols), 1.0, 1001)
+    k, v = caches(n, nkv, cap, 1002)
+    pk, pv = WL.gen_normal((nkv, prefix, D), 1.0, 1004), WL.gen_normal((nkv, prefix, D), 1.0, 1005)
+    kg, vg = k.cuda(), v.cuda()
+    ws = T.decode_workspace(n, h, tp, prefix)
+    args = (pk.cuda(), pv.cuda()) if prefix else (None, None)
+    out = T.sharded_prefix_decode(qkv.cuda(), h, tp, *args, pos.cuda(), kg, vg, ws)
+    kr, vr = f64(k).copy(), f64(v).copy()
+    close(out, *O.cached_decode(qkv, hq, hkv, D, tp, pos.tolist(), cap, 0, kr, vr, f64(pk), f64(pv)))
+    assert np.array_equal(f64(kg), kr) and np.array_equal(f64(vg), vr)
+
+
+@pytest.mark.parametrize("hq", [96, 128, 160])
+def test_decode_many_query_heads_per_kv_head(T, hq):
+    h, n, cap, P = T.Heads(hq, 1, D), 3, 70, 150
+    cols = (hq + 2) * D
+    qkv, (k, v) = WL.gen_normal((n, cols), 1.0, 1011), caches(n, 1, cap, 1012)
+    pk, pv = WL.gen_normal((1, P, D), 1.0, 1014), WL.gen_normal((1, P, D), 1.0, 1015)
+    pos = torch.tensor([0, 69, 33], dtype=torch.int32)
+    ws = T.decode_workspace(n, h, 1, P)
+    out = T.sharded_window_decode(qkv.cuda(), h, 1, pos.cuda(), cap, k.cuda(), v.cuda(), ws)
+    close(out, *O.cached_decode(qkv, hq, 1, D, 1, pos.tolist(), cap, 0, f64(k).copy(), f64(v).copy()))
+    call = lambda: T.sharded_prefix_decode(qkv.cuda(), h, 1, pk.cuda(), pv.cuda(), pos.cuda(), k.cuda(), v.cuda(), ws)
+    if hq > 128:
+        with pytest.raises(T.TpsError) as e:
+            call()
+        assert e.value.status == T.TPS_ERR_UNIMPLEMENTED
+    else:
+        close(call(), *O.cached_decode(qkv, hq, 1, D, 1, pos.tolist(), cap, 0, f64(k).copy(), f64(v).copy(), f64(pk), f64(pv)))
+
+
+def test_cache_offsets_beyond_32_bits(T):
+    """Caches of 5 GB each: the last sequence's slots lie behind 2^32 bytes and 2^31 elements."""
+    hq, hkv, tp, n, cap, ns, W = 4, 2, 1, 5, 2_000_000, 3, 300
+    h = T.Heads(hq, hkv, D)
+    nkv, cols = geom(hq, hkv, tp)
+    kg = torch.zeros(n, nkv, cap, D, dtype=torch.bfloat16, device="cuda")
+    vg = torch.zeros(n, nkv, cap, D, dtype=torch.bfloat16, device="cuda")
+    S = 400
+    qkv = WL.gen_normal((n * S, cols), 1.0, 1021)
+    first = [0, cap - 200, 10 * cap + 7, 1_999_000, cap - 1]
+    pos = torch.tensor(first, dtype=torch.int32, device="cuda")
+    T.sharded_kv_append(qkv.cuda(), n, S, h, tp, kg, vg, pos=pos, nsink=ns)
+    new = WL.gen_normal((n, cols), 1.0, 1022)
+    ws = T.decode_workspace(n, h, tp)
+    out = T.sharded_window_decode(new.cuda(), h, tp, pos + S, W, kg, vg, ws, nsink=ns)
+    x = O.to_f64(qkv).reshape(n, S, cols)
+    y = O.to_f64(new)
+    for b in range(n):
+        vis = [t - first[b] for t in range(first[b] + S - W + 1, first[b] + S)]     # the window's older tokens
+        sinks = [t - first[b] if first[b] <= t else None for t in range(ns)]        # None: never written, zeros
+        for hd in range(hq):
+            kc, vc = (hq + hd // 2) * D, (hq + hkv + hd // 2) * D
+            pick = lambda c: np.stack([np.zeros(D) if i is None else x[b, i, c:c + D] for i in sinks + vis] + [y[b, c:c + D]])
+            ref, mag = O.attend(y[b, hd * D:(hd + 1) * D], pick(kc), pick(vc))
+            close(out[b, hd * D:(hd + 1) * D], ref, mag, f"sequence {b}")
+
+
+def test_decode_steps_without_a_pause(T):
+    """Many steps in a row, with and without a prefix, on one workspace: every one gives the
+    first one's bits."""
+    hq, hkv, tp, n, cap, P = 32, 8, 8, 24, 300, 4000
+    h = T.Heads(hq, hkv, D)
+    nkv, cols = geom(hq, hkv, tp)
+    g = torch.Generator().manual_seed(3)
+    qkv, (k, v) = WL.gen_normal((n, cols), 1.0, 1031).cuda(), [t.cuda() for t in caches(n, nkv, cap, 1032)]
+    pk, pv = WL.gen_normal((nkv, P, D), 1.0, 1034).cuda(), WL.gen_normal((nkv, P, D), 1.0, 1035).cuda()
+    pos = torch.randint(-1, cap, (n,), generator=g, dtype=torch.int32).cuda()
+    ws = T.decode_workspace(n, h, tp, P)
+    both = lambda: (T.sharded_prefix_decode(qkv, h, tp, pk, pv, pos, k, v, ws),
+                    T.sharded_window_decode(qkv, h, tp, pos, cap - 2, k, v, ws, nsink=2))
+    first = both()
+    later = [both() for _ in range(60)]
+    torch.cuda.synchronize()
+    for a, b in later:
+        assert torch.equal(a, first[0]) and torch.equal(b, first[1])
+    assert T.tps_sync_status(ws) == T.TPS_OK
+
+
+def test_two_streams_at_once(T):
+    """Decode steps and draws on two streams, each with its own workspace."""
+    hq, hkv, tp, n, cap = 32, 8, 8, 16, 900
+    h = T.Heads(hq, hkv, D)
+    nkv, cols = geom(hq, hkv, tp)
+    sets = []
+    for i in range(2):
+        qkv, (k, v) = WL.gen_normal((n, cols), 1.0, 1041 + i).cuda(), [t.cuda() for t in caches(n, nkv, cap, 1043 + 2 * i)]
+        pos = torch.randint(0, cap, (n,), generator=torch.Generator().manual_seed(i), dtype=torch.int32).cuda()
+        logits, u, _ = rows(8, 33008, 2.0, 1050 + i)
+        sets.append((qkv, k, v, pos, T.decode_workspace(n, h, tp), logits.cuda(), u.cuda(), torch.cuda.Stream()))
+    run = lambda s, st: (T.sharded_window_decode(s[0], h, tp, s[3], cap, s[1], s[2], s[4], stream=st),
+                         T.logits_sample(s[5], s[6], top_p=torch.full((8,), 0.9, device="cuda"), stream=st)[0])
+    want = [run(s, None) for s in sets]
+    torch.cuda.synchronize()
+    got = [[run(s, s[7]) for s in sets] for _ in range(20)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for (a, i), (b, j) in zip(pair, want):
+            assert torch.equal(a, b) and torch.equal(i, j)
