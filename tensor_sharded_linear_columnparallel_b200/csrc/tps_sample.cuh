@@ -150,7 +150,6 @@ struct SampleSmem {
   u64 top[8], have[8];
   SampleCmd cmd;
   int listed;                  // first CTA: list entries handed out
-  int unused;
   float fred[2 * kSampleMaxWarps];
 };
 
@@ -231,6 +230,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
     u64 none = 0;
     return cluster_all2(v, none);
   };
+  cluster_arrive();                            // waited for before the first access to another CTA's memory
   griddep_wait();
   const float T = a.temperature ? a.temperature[row] : 1.0f;
   const float pf = a.top_p ? a.top_p[row] : 1.0f;
@@ -290,6 +290,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
   }
   // also: how many threads have a logit above -inf
   const int finite = __syncthreads_count(most > -INFINITY);
+  cluster_wait();                              // every CTA of the cluster runs
   if (tid < cs) {
     st_cluster_u64(remote(&s.top[cr], tid), static_cast<u64>(__float_as_uint(mx)) << 32 | __float_as_uint(mn));
     st_cluster_u64(remote(&s.have[cr], tid), static_cast<u64>(finite));
