@@ -378,8 +378,8 @@ TPS_API int sharded_kv_append(const void* qkv, int64_t nseq, int64_t seqlen, con
  *   [nseq, hq*d], the input layout of the o_proj row pack. A row with pos[b] < 0 is an
  *   unused slot of the batch: its caches stay as they are and its output is zero.
  *   ws: device workspace of at least tps_decode_workspace_bytes(nseq, heads, tp, 0)
- *   bytes, zero-filled before its first use and left ready for the next call; calls
- *   that share one are ordered by their stream. The positions are read on the device:
+ *   bytes, zero-filled before its first use and left ready for the next call of either
+ *   kind and any size; calls that share one are ordered by their stream. The positions are read on the device:
  *   a captured graph replays with the positions of its replay.
  *   Softmax in fp32, weights rounded to bf16 for the product with V (fp32 accumulation).
  *   Errors as sharded_kv_append, and TPS_ERR_WORKSPACE.

@@ -1177,7 +1177,7 @@ int cache_geom(const tps_heads* heads, int tp, int64_t nsink, int64_t cap, HeadM
   return TPS_OK;
 }
 
-// Workspace of a decode step: header, item counters, the decode kernel's parts, then the
+// Workspace of a decode step: header, a counter per CTA, the decode kernel's parts, then the
 // prefix kernel's max / sum and parts.
 struct DecodeWs {
   int nch;                      // chunks of 16 query heads per KV head slot
@@ -1191,7 +1191,7 @@ DecodeWs decode_ws(int64_t nseq, const HeadMap& hm, int64_t nkv, int64_t prefix_
   w.nch = (G + 15) / 16;
   size_t at = kHdr;
   w.counters = at;
-  at += round256(static_cast<size_t>(nseq) * nkv * w.nch * 4);
+  at += round256(static_cast<size_t>(sms) * 4);   // at the same place whatever the sizes: zero between any two calls
   w.parts = at;
   at += round256(static_cast<size_t>(sms) * 2 * tps::kDecPartFloats * 4);
   if (prefix_len > 0 && G <= 128) {

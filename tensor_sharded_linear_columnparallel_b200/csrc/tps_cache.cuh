@@ -72,7 +72,9 @@ __global__ void __launch_bounds__(kAppendThreads) tps_kv_append_kernel(const KvA
 // with some blocks' room ahead of it for what it costs besides its stream, and every CTA
 // (one per SM) takes an equal part of the line, wherever that begins and ends. An item
 // cut by a border leaves its parts (running max, sum, unnormalised output, fp32) in the
-// workspace, and the CTA that finishes last merges them; its counter returns to zero.
+// workspace, and the CTA that finishes last merges them. A CTA's part ends in at most one
+// item that goes on behind it, so the item's counter is that of the CTA which has its first
+// block: a place in the workspace that no size moves. It returns to zero.
 // Behind a shared prefix every item leaves a part, to be merged with the prefix kernel's.
 // Merging waits until the CTA's stream has ended and then uses all its warps, one output
 // row each: done where an item ends, it held the stream up (window_decode of 32 sequences
@@ -198,8 +200,8 @@ struct DecWalk {
     do {
       if (at >= w.w1 || w.w0 == w.w1) return false;
       while (k == a.nkv * a.nch || v.blocks() == 0) {           // the next sequence with blocks
+        if (++b >= a.nseq) return false;                        // never, unless the positions change meanwhile
         v = dec_view(a, tnext);
-        ++b;
         tnext = b + 1 < a.nseq ? __ldcg(a.pos + b + 1) : -1;
         k = 0;
       }
@@ -345,7 +347,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kDecOffBar + 160);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + kDecOffBar + 164);
   volatile int* never_flag = reinterpret_cast<volatile int*>(gbase + kDecOffBar + 168);
-  int* last_flag = reinterpret_cast<int*>(gbase + kDecOffBar + 172);    // [4]: cut items, their other CTAs
+  int* last_flag = reinterpret_cast<int*>(gbase + kDecOffBar + 172);    // [4]: cut items' counters, their other CTAs
   DecWork* sWork = reinterpret_cast<DecWork*>(gbase + kDecOffBar + 192);
   static_assert(192 + sizeof(DecWork) <= 256, "barrier block");
   int* scan = reinterpret_cast<int*>(gbase + kDecOffRed);   // [kDecWarps] before the roles start
@@ -753,8 +755,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         float* slot = dec_part(a, w, it, static_cast<int>(blockIdx.x));
         if (!it.whole() && warp == 2 && lane == 0) {   // counted below, when the part is written
           const int k = it.s <= w.w0 ? 0 : 1;
-          last_flag[k] = (it.b * a.nkv + it.g) * a.nch + it.ch;
-          last_flag[2 + k] = dec_owner(w, it.s + it.nb - 1) - dec_owner(w, it.s);
+          last_flag[k] = dec_owner(w, it.s);
+          last_flag[2 + k] = dec_owner(w, it.s + it.nb - 1) - last_flag[k];
         }
 #pragma unroll
         for (int h = 0; h < kDecHeads; ++h)
@@ -783,11 +785,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     // the cut items are this CTA's first and last: two threads count them, and put 1 where
     // the last of an item's CTAs is this one
     if (lane == 0 && warp < 2) {
-      const int item = last_flag[warp];
+      const int first = last_flag[warp];
       bool last = false;
-      if (item >= 0) {
-        last = atomicAdd(a.counters + item, 1) == last_flag[2 + warp];
-        if (last) a.counters[item] = 0;                // left zero for the next call
+      if (first >= 0) {
+        last = atomicAdd(a.counters + first, 1) == last_flag[2 + warp];
+        if (last) a.counters[first] = 0;               // left zero for the next call
       }
       __threadfence();
       last_flag[warp] = last;

@@ -134,7 +134,7 @@ struct DecodeArgs {
   int ldo;
   int nch;                         // chunks of 16 query heads per KV head slot
   int room;                        // places of an item in the line of blocks besides its blocks (tps_cache.cuh)
-  int* counters;                   // [nseq*nkv*nch] CTAs that have left their part of an item, zero between calls
+  int* counters;                   // [grid] CTAs that have left their part of an item, zero between calls
   float* parts;                    // [grid][2][kDecPartFloats]: 16 x 128 output, 16 max, 16 sum
   float* item_parts;               // [nseq*nkv*nch][kDecPartFloats], behind a prefix
   const float *prefix_parts, *prefix_ml;   // parts of the prefix kernel (see AttnArgs), or null

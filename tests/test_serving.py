@@ -600,6 +600,25 @@ def test_decode_more_sequences_than_threads(T, prefix):
     assert np.array_equal(f64(kg), kr) and np.array_equal(f64(vg), vr)
 
 
+def test_decode_workspace_shared_by_calls_of_other_sizes(T):
+    """One workspace, made for the largest of them, serves calls of any sizes in turn."""
+    hq, hkv, tp, P = 16, 4, 2, 300
+    nkv, cols = geom(hq, hkv, tp)
+    h = T.Heads(hq, hkv, D)
+    sizes = [(1, 5000, 0), (900, 260, 0), (3, 2000, P), (900, 150, P), (2, 9000, 0), (50, 900, 0)]
+    shared = torch.zeros(max(T.tps_decode_workspace_bytes(n, h, tp, P) for n, _, _ in sizes), dtype=torch.uint8, device="cuda")
+    pk, pv = WL.gen_normal((nkv, P, D), 1.0, 1101).cuda(), WL.gen_normal((nkv, P, D), 1.0, 1102).cuda()
+    for n, cap, prefix in sizes:
+        qkv = WL.gen_normal((n, cols), 1.0, 1103).cuda()
+        k, v = (x.cuda() for x in caches(n, nkv, cap, 1104))
+        pos = torch.full((n,), cap - 1, dtype=torch.int32, device="cuda")
+        args = (pk, pv) if prefix else (None, None)
+        got = T.sharded_prefix_decode(qkv, h, tp, *args, pos, k, v, shared)
+        want = T.sharded_prefix_decode(qkv, h, tp, *args, pos, k, v, T.decode_workspace(n, h, tp, prefix))
+        assert torch.equal(got, want), (n, cap, prefix)
+
+
+
 @pytest.mark.parametrize("hq", [96, 128, 160])
 def test_decode_many_query_heads_per_kv_head(T, hq):
     h, n, cap, P = T.Heads(hq, 1, D), 3, 70, 150
