@@ -508,28 +508,35 @@ int launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs
   return launch_with_smem(tps_decode_kernel, &attr_done, kDecThreads, kDecSmemBytes, grid, st, 1, kDecSmemBytes, tk, tv, a);
 }
 
-// CTAs per row: as few as hold it at 16384 tokens each, and more, down to 4096 tokens each,
-// while the SMs are not covered. Few rows go by latency: 1024 threads shorten the passes over
-// a CTA's part. Many go by throughput: of CTAs with 256 threads four fit an SM (three with
-// fp32 logits), so a batch of 64 rows of a 128256-token vocabulary runs in one wave.
 template <class E>
-static int launch_sample_type(const SampleArgs& a, int cs, int num_sms, cudaStream_t st) {
+static int launch_sample_type(const SampleArgs& a, int cs, int threads, cudaStream_t st) {
   const int smem = sample_smem_bytes(a.slice, a.f32);
   const int max_smem = sample_smem_bytes(static_cast<int>(kSampleMaxVocab / 8), a.f32);
   static unsigned long long attr_done[2] = {0ull, 0ull};
-  if (static_cast<long long>(a.m) * cs <= num_sms && a.slice > 2048)
-    return launch_with_smem(tps_sample_kernel<E, 1024, 1>, &attr_done[0], 1024, smem, a.m * cs, st, cs, max_smem, a);
-  return launch_with_smem(tps_sample_kernel<E, 256, 4>, &attr_done[1], 256, smem, a.m * cs, st, cs, max_smem, a);
+  return threads == 256
+             ? launch_with_smem(tps_sample_kernel<E, 256, 4>, &attr_done[1], 256, smem, a.m * cs, st, cs, max_smem, a)
+             : launch_with_smem(tps_sample_kernel<E, 512, 2>, &attr_done[0], 512, smem, a.m * cs, st, cs, max_smem, a);
 }
 
+// CTAs per row: as few as hold it at 32768 tokens each, and twice as many, down to 4096 tokens
+// each, while all of them still have an SM of their own: a row's passes are shorter, but clusters
+// of eight are placed worse and wait longer for one another (rows of 128256 bf16 logits with
+// filters of all kinds, four or eight CTAs: 8 rows 32 or 24 us, 32 rows 37 or 34, 64 rows 43 or
+// 49; behind a GEMM, fp32, 32 rows: 204 or 218 us with it). 512 threads; 256 for short parts,
+// which leave most of 512 idle, and for many fp32 rows, in eight CTAs, of whose 64 KB three fit
+// an SM where one of 128 KB does (256 rows: 159 us, 177 in four CTAs of 512 threads; 64: 53 and
+// 62, but behind a GEMM 237 and 225 with it).
 int launch_sample(const SampleArgs& a, int num_sms, cudaStream_t st) {
   int cs = 1;
-  while (cs < 8 && a.V > cs * 16384) cs *= 2;
-  while (cs < 8 && static_cast<long long>(a.m) * cs < num_sms && a.V > cs * 4096) cs *= 2;
+  while (cs < 8 && a.V > cs * 32768) cs *= 2;
+  while (cs < 8 && 2LL * a.m * cs <= num_sms && a.V > cs * 4096) cs *= 2;
+  const bool split = a.f32 && cs < 8 && a.V > cs * 16384 && static_cast<long long>(a.m) * cs > 2LL * num_sms;
+  if (split) cs *= 2;
   if (static_cast<long long>(a.m) * cs > 0x7fffffffLL) return -6;
   SampleArgs b = a;
   b.slice = ((a.V + cs - 1) / cs + 7) / 8 * 8;
-  return a.f32 ? launch_sample_type<float>(b, cs, num_sms, st) : launch_sample_type<__nv_bfloat16>(b, cs, num_sms, st);
+  const int threads = split || b.slice <= 2048 ? 256 : 512;
+  return a.f32 ? launch_sample_type<float>(b, cs, threads, st) : launch_sample_type<__nv_bfloat16>(b, cs, threads, st);
 }
 
 int launch_gemm(int swap, int bn, int dual, const CUtensorMap& tx, const CUtensorMap& tw, const GemmArgs& a,

@@ -18,15 +18,21 @@
 //    octave of bins, so that a bin's 32-bit sum keeps its relative precision. It tells the
 //    bin of the cut but for roundings; the one pass that computes the exact weights, of all
 //    tokens and of those above the bin, tells whether it is that bin or the one beside it.
-// The tokens of those bins go to a list in the first CTA, which takes the cut from exact sums,
-// for top-k that of top-p too, and with up to 256 tokens it draws there: each token finds
-// its own place by comparing itself with the others, without a sort. Bins are equal parts
-// of the logits within 32 T of the maximum (what lies below has no weight). Where they hold
-// more than the list (equal logits, one far outlier that stretches them), the threshold is
-// found bit by bit from passes over shared memory.
+// The tokens of those bins go to a list, each CTA's part first in its own memory, then all in
+// the first CTA, which takes the cut from exact sums (sample_select), for top-k that of top-p
+// too. With a list of up to 256 tokens from the top it draws there: each token finds its own place
+// by comparing itself with the others, without a sort. After a cut to p it sends the weights
+// of the list's kept tokens to the warps whose tokens they are, so that the draw needs no pass
+// over the row. Bins are equal parts of the logits within 32 T of the maximum (what lies below
+// has no weight). Where they hold more than the list (equal logits, one far outlier that
+// stretches them), the threshold is found bit by bit from passes over shared memory.
 //
-// Bound by latency for few rows (five cluster barriers of about a microsecond), and by the
-// 64-bit exponentials and the shared-memory atomics of the weight histogram for many.
+// Bound by latency for few rows: of the 46,000 cycles of one of 8 rows of 128256 bf16 logits cut
+// to p (512 threads, eight CTAs), 4,000 load it, 7,600 fill the histogram, 3,700 find the bin,
+// 10,000 sum the exact weights, 8,000 cut the list, and six cluster barriers take about 1,100
+// each. For many rows by the instructions of the two passes: an approximate and a 64-bit
+// exponential and a shared-memory atomic per token. With all filters and 64 rows 43 us, where
+// reading the logits takes 2.5.
 #pragma once
 
 #include <cstddef>
@@ -40,14 +46,13 @@ constexpr int kSampleMaxWarps = 32;
 constexpr int kSampleBins = 1024;
 constexpr int kSampleList = 1024;              // entries of the candidate list, whose second half overlays the histogram
 constexpr u64 kSampleOne = 1ull << 44;         // weight of the largest logit
+constexpr int kSampleFew = 64;                 // entries that sample_select compares with one another
 constexpr int kSampleSmall = 256;              // kept tokens that the first CTA draws from by itself
 
-__device__ __forceinline__ uint32_t atomic_add_cluster_u32(uint32_t addr, uint32_t x) {
-  uint32_t v;
-  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(v) : "r"(addr), "r"(x) : "memory");
-  return v;
+__device__ __forceinline__ void atomic_add_cluster_u64(uint32_t addr, u64 x) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;" ::"r"(addr), "l"(x) : "memory");
 }
-// N consecutive words of another CTA's shared memory (N = 1 or 4).
+// N consecutive words of another CTA's shared memory (N = 2 or 4).
 template <int N>
 __device__ __forceinline__ void ld_cluster(uint32_t addr, uint32_t (&v)[N]) {
   if constexpr (N == 4)
@@ -56,7 +61,12 @@ __device__ __forceinline__ void ld_cluster(uint32_t addr, uint32_t (&v)[N]) {
                  : "r"(addr)
                  : "memory");
   else
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v[0]) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ u64 ld_cluster_u64(uint32_t addr) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
@@ -125,11 +135,17 @@ __device__ __forceinline__ u64 sample_weight(float x, const SampleRow& r) {
          static_cast<uint32_t>(__double2loint(m));
 }
 
+// A float in [0, 2^23) rounded to an integer, and an integer as a float, by an addition of 2^23:
+// the conversions go through the unit of the exponential, which bounds the pass over the row.
+__device__ __forceinline__ uint32_t sample_round(float x) { return __float_as_uint(x + 8388608.0f) - 0x4b000000u; }
+__device__ __forceinline__ float sample_float(uint32_t i) { return __uint_as_float(i + 0x4b000000u) - 8388608.0f; }
+
 // Bin of a logit: 0 holds the largest, the last one everything beyond.
 __device__ __forceinline__ int sample_bin(float x, const SampleRow& r) {
-  return static_cast<int>(fminf((r.mxf - x) * r.bin_scale, static_cast<float>(kSampleBins - 1)));
+  return static_cast<int>(sample_round(fminf((r.mxf - x) * r.bin_scale, static_cast<float>(kSampleBins - 1))));
 }
-// Weights of bin b are below 2^(16 + shift): the bin spans less than one octave of weights.
+// Weights of bin b are below 2^(15.1 + shift): the bins of an octave, and half a bin (at most
+// 1/32 octave) of the one before.
 __device__ __forceinline__ int sample_shift(int b, const SampleRow& r) { return max(0, 29 - (b >> r.octave)); }
 
 enum { SAMPLE_CUT, SAMPLE_DRAWN, SAMPLE_SHORT, SAMPLE_DOWN, SAMPLE_UP };   // threshold C; row finished; list too
@@ -148,13 +164,22 @@ struct SampleSmem {
   u64 part[2][8];              // values that the CTAs of the cluster exchange, two in turn
   u64 part2[2][8];
   u64 top[8], have[8];
+  u64 wsum[kSampleMaxWarps];   // after a cut to p: weight of the warps' drawable tokens of the list
   SampleCmd cmd;
-  int listed;                  // first CTA: list entries handed out
+  int listed;                  // entries of this CTA's part of the list
+  int members;                 // first CTA, sample_select: what is left of the list
+  u64 pivot[32], few[kSampleFew], found;
+  uint32_t bucket[2][33];
   float fred[2 * kSampleMaxWarps];
 };
 
 constexpr int kSampleHead = (static_cast<int>(sizeof(SampleSmem)) + 15) / 16 * 16;
 constexpr int sample_smem_bytes(int slice, int f32) { return kSampleHead + kSampleBins * 8 + slice * (f32 ? 4 : 2); }
+
+template <bool B>
+struct SampleFlag {
+  static constexpr bool value = B;
+};
 
 template <class T, class Op>
 __device__ __forceinline__ T sample_warp_reduce(T v, Op op) {
@@ -194,6 +219,84 @@ __device__ __forceinline__ u64 sample_block_scan(u64 v, u64& total, SampleSmem& 
   return __shfl_sync(0xffffffffu, ws - w, warp) + incl - v;
 }
 
+// The entry v of a list (BPT per thread, those with a weight w) with which the running sum of
+// the weights, from the largest entry down and beginning at S, reaches target: S < target <=
+// S + all weights. 32 entries cut the list into 33 buckets; the one that has the entry (a 33rd of
+// the list, give or take) is what is left, until few enough are left to compare each with all.
+// Sums are exact, as two halves of 22 bits of up to 993 weights in a bucket. Sorting the
+// list instead took 55 steps of 330 cycles for 1024 entries, 9 us; this takes 3 to 5.
+template <int THREADS, int BPT>
+__device__ __forceinline__ u64 sample_select(const u64 (&v)[BPT], const u64 (&w)[BPT], u64 S, double target, u64* list,
+                                             SampleSmem& s) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  bool in[BPT];
+#pragma unroll
+  for (int j = 0; j < BPT; ++j) in[j] = w[j] > 0;
+  for (;;) {
+    __syncthreads();
+    if (tid == 0) s.members = 0;
+    if (tid < 66) s.bucket[tid >= 33][tid >= 33 ? tid - 33 : tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < BPT; ++j) {
+      const uint32_t m = __ballot_sync(0xffffffffu, in[j]);
+      int at = 0;
+      if (lane == 0 && m) at = atomicAdd(&s.members, __popc(m));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1u));
+      if (in[j]) {
+        list[at] = v[j];
+        if (at < kSampleFew) s.few[at] = w[j];
+      }
+    }
+    __syncthreads();
+    const int n = s.members;
+    if (n <= kSampleFew) break;
+    if (tid < 32) {
+      const u64 mine = list[lane * n >> 5];
+      int place = 0;
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) place += list[i * n >> 5] > mine;
+      s.pivot[place] = mine;
+    }
+    __syncthreads();
+    int b[BPT];
+#pragma unroll
+    for (int j = 0; j < BPT; ++j) {
+      b[j] = 0;                                // pivots above the entry
+      if (in[j]) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          if (s.pivot[b[j] + o - 1] > v[j]) b[j] += o;
+        if (s.pivot[b[j]] > v[j]) ++b[j];
+        atomicAdd(&s.bucket[0][b[j]], static_cast<uint32_t>(w[j]) & 0x3fffffu);
+        atomicAdd(&s.bucket[1][b[j]], static_cast<uint32_t>(w[j] >> 22));
+      }
+    }
+    __syncthreads();
+    const u64 mine = s.bucket[0][lane] + (static_cast<u64>(s.bucket[1][lane]) << 22);
+    u64 incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, static_cast<double>(S + incl) >= target);
+    const int sel = hit ? __ffs(hit) - 1 : 32;
+    S += __shfl_sync(0xffffffffu, hit ? incl - mine : incl, hit ? sel : 31);
+#pragma unroll
+    for (int j = 0; j < BPT; ++j) in[j] = in[j] && b[j] == sel;
+  }
+  if (tid < s.members) {
+    const u64 mine = list[tid];
+    u64 before = S;
+#pragma unroll 4
+    for (int i = 0; i < s.members; ++i) before += list[i] > mine ? s.few[i] : 0;
+    if (static_cast<double>(before) < target && static_cast<double>(before + s.few[tid]) >= target) s.found = mine;
+  }
+  __syncthreads();
+  return s.found;
+}
+
 template <class E, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleArgs a) {
   constexpr int WARPS = THREADS / 32;
@@ -203,7 +306,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
   u64* list = reinterpret_cast<u64*>(smem_raw + kSampleHead);
   uint32_t* hist = reinterpret_cast<uint32_t*>(list + kSampleList / 2);
   E* xs = reinterpret_cast<E*>(hist + kSampleBins);
-  static_assert(kSampleList * 8 == kSampleBins * 8 && kSampleSmall <= THREADS && (BPT == 1 || BPT == 4),
+  static_assert(kSampleList * 8 == kSampleBins * 8 && kSampleSmall <= THREADS && (BPT == 2 || BPT == 4),
                 "shared memory layout");
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -248,22 +351,29 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
   float mx = -INFINITY, mn = INFINITY;         // neither takes a NaN
   const E* src = static_cast<const E*>(a.logits) + static_cast<long long>(row) * a.V + i0;
   constexpr int EPV = 16 / sizeof(E);
-#pragma unroll 8
-  for (int v = tid; v < n / EPV; v += THREADS) {
-    const uint4 q = __ldcs(reinterpret_cast<const uint4*>(src) + v);
-    reinterpret_cast<uint4*>(xs)[v] = q;
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  for (int v0 = tid; v0 < n / EPV; v0 += 8 * THREADS) {
+    uint4 in[8];                               // 8 loads in flight, in the last round too
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float x = __uint_as_float(EPV == 4 ? w[j] : w[j] & 0xffff0000u);
-      const float y = EPV == 4 ? x : __uint_as_float(w[j] << 16);
-      mx = fmaxf(fmaxf(mx, x), y);
-      mn = fminf(fminf(mn, x), y);
+    for (int c = 0; c < 8; ++c)
+      if (v0 + c * THREADS < n / EPV) in[c] = __ldcs(reinterpret_cast<const uint4*>(src) + v0 + c * THREADS);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (v0 + c * THREADS >= n / EPV) break;
+      reinterpret_cast<uint4*>(xs)[v0 + c * THREADS] = in[c];
+      const uint32_t w[4] = {in[c].x, in[c].y, in[c].z, in[c].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = __uint_as_float(EPV == 4 ? w[j] : w[j] & 0xffff0000u);
+        const float y = EPV == 4 ? x : __uint_as_float(w[j] << 16);
+        mx = fmaxf(fmaxf(mx, x), y);
+        mn = fminf(fminf(mn, x), y);
+      }
     }
   }
   float most = mx;                             // this thread's largest
   for (int j = tid; j < kSampleBins; j += THREADS) hist[j] = 0;
   if (tid == 0) s.listed = 0;
+  if (tid < WARPS) s.wsum[tid] = 0;
   mx = sample_warp_reduce(mx, [](float x, float y) { return fmaxf(x, y); });
   mn = sample_warp_reduce(mn, [](float x, float y) { return fminf(x, y); });
   if (lane == 0) s.fred[warp] = mx, s.fred[WARPS + warp] = mn;
@@ -388,11 +498,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
     return t;
   };
   // A warp has a contiguous part [j0, j1) of the CTA's tokens.
-  const int per = (((n + WARPS - 1) / WARPS) + 127) & ~127;
+  auto warp_part = [](int n) { return (((n + WARPS - 1) / WARPS) + 127) & ~127; };
+  const int per = warp_part(n);
   const int j0 = min(n, warp * per), j1 = min(n, j0 + per);
-  // After a cut to p: weight of the warp's drawable tokens in bins before lo (behind hi none is left).
+  // After a cut to p: weight of the warp's drawable tokens, those before the list and those of the list.
   u64 base = 0;
-  int lo = 0, hi = kSampleBins;
+  bool summed = false;
   auto set_threshold = [&](u64 rank) {
     cx = sample_unkey(static_cast<uint32_t>(rank >> 32));    // always within the tokens kept so far
     ci = static_cast<int>(0xffffffffu - static_cast<uint32_t>(rank));
@@ -416,7 +527,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
       each([&](float x, int i) {
         const int b = sample_bin(x, r);
         // 2^(44 - y - shift), at most 2^15 but for a rounding: 49152 of them fit 32 bits
-        const uint32_t m = __float2uint_rn(ex2_approx(static_cast<float>(44 - sample_shift(b, r)) - (r.mxf - x) * cf));
+        const uint32_t m = sample_round(ex2_approx(sample_float(44 - sample_shift(b, r)) - (r.mxf - x) * cf));
         if (keeps(x, i) && m) atomicAdd(hist + b, m);
       });
       __syncthreads();
@@ -476,8 +587,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
     do {
       u64 above = 0, all = 0;                    // weight above the list, and of all tokens
       auto enlist = [&](float x, int i) {
-        const uint32_t at = atomic_add_cluster_u32(remote(&s.listed, 0), 1u);
-        if (at < kSampleList) st_cluster_u64(remote(list + at, 0), sample_rank(x, i));
+        const int at = atomicAdd(&s.listed, 1);
+        if (at < kSampleList) list[at] = sample_rank(x, i);
       };
       if (k > 0 && !cmd.skip) {
         each([&](float x, int i) {
@@ -487,37 +598,61 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
         });
       } else if (k == 0) {
         base = 0;
-        for (int j = j0 + 4 * lane; j < j1; j += 128) {
-          float x[4];
-          sample_get4(xs, j >> 2, x);
+        auto pass = [&](auto plain) {            // plain: no other filter
+          for (int j = j0 + 4 * lane; j < j1; j += 128) {
+            float x[4];
+            u64 w[4];
+            bool in[4];
+            sample_get4(xs, j >> 2, x);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int b = sample_bin(x[q], r);
-            const u64 w = keeps(x[q], i0 + j + q) ? sample_weight(x[q], r) : 0;
-            const u64 wa = b < cmd.lo ? w : 0;
-            all += w;
-            above += wa;
-            base += survives(wa) ? wa : 0;
-            if (b == cmd.lo && w) enlist(x[q], i0 + j + q);
+            for (int q = 0; q < 4; ++q) {        // four exponentials side by side: no branch among them
+              const int b = sample_bin(x[q], r);
+              w[q] = sample_weight(x[q], r);
+              if (!plain.value) w[q] = keeps(x[q], i0 + j + q) ? w[q] : 0;
+              const u64 wa = b < cmd.lo ? w[q] : 0;
+              all += w[q];
+              above += wa;
+              if (!plain.value) base += survives(wa) ? wa : 0;
+              in[q] = b == cmd.lo && w[q];
+            }
+            if (in[0] | in[1] | in[2] | in[3])
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if (in[q]) enlist(x[q], i0 + j + q);
           }
-        }
+          if (plain.value) base = above;
+        };
+        if (r.q == 0 && cx == -INFINITY) pass(SampleFlag<true>{});
+        else pass(SampleFlag<false>{});
         base = sample_warp_reduce(base, [](u64 x, u64 y) { return x + y; });
-        lo = cmd.lo;
-        hi = cmd.hi;
         above = sample_block_sum<THREADS>(above, s);
         all = sample_block_sum<THREADS>(all, s);
       }
-      if (cr > 0)                                // for another cut
-        for (int j = tid; j < kSampleBins; j += THREADS) hist[j] = 0;
+      __syncthreads();
+      if (tid == 0) st_cluster_u64(remote(&s.have[cr], 0), static_cast<u64>(s.listed));
       all = cluster_all2(all, above);
       if (cmd.skip) {
-        if (cr == 0)
-          for (int j = tid; j < kSampleBins; j += THREADS) hist[j] = 0;
+        for (int j = tid; j < kSampleBins; j += THREADS) hist[j] = 0;
         __syncthreads();
         return after;
       }
       if (cr == 0) {
-        const int len = s.listed;
+        // the other CTAs' parts of the list behind this one's
+        int end[8], len = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          if (q < cs) len += static_cast<int>(s.have[q]);
+          end[q] = len;
+        }
+        if (len <= kSampleList)
+          for (int e = end[0] + tid; e < len; e += THREADS) {
+            int q = 0, from = 0;
+#pragma unroll
+            for (int o = 0; o < 7; ++o)
+              if (e >= end[o]) q = o + 1, from = end[o];
+            list[e] = ld_cluster_u64(remote(list + (e - from), q));
+          }
+        __syncthreads();
         if (len > kSampleList) {
           tell(SAMPLE_SHORT);
         } else if (whole && len <= kSampleSmall) {
@@ -562,56 +697,47 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
           if (in && half == 0 && upto > t && upto - we <= t) draw(static_cast<int>(0xffffffffu - ie), we, tot);
           tell(SAMPLE_DRAWN);
         } else {
-          int m = 32;                            // bitonic sort, descending, padded with zeros
-          while (m < len) m <<= 1;
-          for (int j = len + tid; j < m; j += THREADS) list[j] = 0;
-          __syncthreads();
-          for (int size = 2; size <= m; size <<= 1)
-            for (int d = size >> 1; d > 0; d >>= 1) {
-              for (int j = tid; j < m / 2; j += THREADS) {
-                const int a = 2 * j - (j & (d - 1)), b = a + d;
-                const u64 x = list[a], y = list[b];
-                if ((x < y) == ((a & size) == 0)) list[a] = y, list[b] = x;
-              }
-              // a distance up to 32 stays within the 64 entries of a warp, in this step and the next
-              if (d > 32 || (d == 1 && size >= 64)) __syncthreads();
-              else __syncwarp();
-            }
-          __syncthreads();
-          const int kk = k > 0 ? k - static_cast<int>(cmd.total) : len;   // entries that may stay
-          int last = kk - 1;                     // the last kept one
+          u64 v[BPT], w[BPT], C = 0;
+#pragma unroll
+          for (int j = 0; j < BPT; ++j) v[j] = tid * BPT + j < len ? list[tid * BPT + j] : 0;
           int found = SAMPLE_CUT;
-          if (k == 0 || (whole && by_p)) {
-            u64 w[BPT], sum = 0, tot;            // BPT entries per thread: the weight before each
+          for (bool count = k > 0;; count = false) {
+            u64 sum = 0;                         // to k: entries as they are; to p: those the cut to k left
 #pragma unroll
             for (int j = 0; j < BPT; ++j) {
-              w[j] = tid * BPT + j < kk
-                         ? sample_weight(sample_unkey(static_cast<uint32_t>(list[tid * BPT + j] >> 32)), r) : 0;
+              const bool in = tid * BPT + j < len && v[j] >= C;
+              w[j] = !in ? 0 : count ? 1 : sample_weight(sample_unkey(static_cast<uint32_t>(v[j] >> 32)), r);
               sum += w[j];
             }
-            u64 before = sample_block_scan<THREADS>(sum, tot, s) + above;
-            const double target = p * static_cast<double>(k == 0 ? all : tot);
-            u64 kept = 0;
-#pragma unroll
-            for (int j = 0; j < BPT; ++j) {
-              kept += tid * BPT + j < kk && static_cast<double>(before) < target;
-              before += w[j];
+            double target = static_cast<double>(k) - static_cast<double>(cmd.total);
+            if (!count) {
+              const u64 tot = above + sample_block_sum<THREADS>(sum, s);
+              target = p * static_cast<double>(k == 0 ? all : tot);
+              if (k == 0 && cmd.lo > 0 && static_cast<double>(above) >= target) found = SAMPLE_DOWN;
+              else if (k == 0 && cmd.hi < kSampleBins - 1 && static_cast<double>(tot) < target) found = SAMPLE_UP;
+              if (found != SAMPLE_CUT) break;
+              target = fmin(fmax(target, static_cast<double>(above) + 0.5), static_cast<double>(tot));   // the first always
             }
-            last = max(static_cast<int>(sample_block_sum<THREADS>(kept, s)), 1) - 1;
-            if (k == 0 && cmd.lo > 0 && static_cast<double>(above) >= target) found = SAMPLE_DOWN;
-            else if (k == 0 && cmd.hi < kSampleBins - 1 && static_cast<double>(above + tot) < target) found = SAMPLE_UP;
+            C = sample_select<THREADS, BPT>(v, w, above, target, list, s);
+            if (!count || !whole || !by_p) break;
           }
-          const u64 C = list[last];
-          __syncthreads();
           if (tid < cs) st_cluster_u64(remote(&s.cmd.C, tid), C);
+          if (k == 0 && found == SAMPLE_CUT)
+#pragma unroll
+            for (int j = 0; j < BPT; ++j)
+              if (w[j] && v[j] >= C && survives(w[j])) {
+                const int i = static_cast<int>(0xffffffffu - static_cast<uint32_t>(v[j])), q = i / a.slice;
+                const int nq = min(a.V, (q + 1) * a.slice) - q * a.slice;
+                atomic_add_cluster_u64(remote(&s.wsum[(i - q * a.slice) / warp_part(nq)], q), w[j]);
+              }
           tell(found);
         }
-        __syncthreads();                         // every thread has read `listed` and the list
-        for (int j = tid; j < kSampleBins; j += THREADS) hist[j] = 0;
-        if (tid == 0) s.listed = 0;
       }
       cluster_sync_all();
       result = s.cmd.result;
+      for (int j = tid; j < kSampleBins; j += THREADS) hist[j] = 0;   // the list has been read
+      if (tid == 0) s.listed = 0;
+      __syncthreads();
       const int move = result == SAMPLE_UP ? 1 : result == SAMPLE_DOWN ? -1 : 0;
       cmd.lo += move;
       cmd.hi += move;
@@ -620,10 +746,13 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
     if (result == SAMPLE_SHORT) {
       if (k > 0 && by_thread) return RETRY;
       set_threshold(bisect(k == 0, static_cast<u64>(k), p));
-      base = 0, lo = 0, hi = kSampleBins;
       return after;
     }
     set_threshold(s.cmd.C);
+    if (k == 0) {
+      base += s.wsum[warp];
+      summed = true;
+    }
     return whole ? DRAW : after;
   };
   const bool by_p = p < 1.0;
@@ -651,15 +780,13 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
         mine += (f(x[0], j) + f(x[1], j + 1)) + (f(x[2], j + 2) + f(x[3], j + 3));
     }
   };
-  if (hi < kSampleBins)                        // the tokens above the list are in `base`
-    part([&](float x, int j) {
-      u64 w = 0;
-      if (keeps(x, i0 + j) && sample_bin(x, r) >= lo) w = kept(x, j);
-      return w;
-    });
-  else if (r.q > 0 || cx > -INFINITY) part(kept);
-  else part([&](float x, int) { return sample_weight(x, r); });
-  mine = sample_warp_reduce(mine, [](u64 x, u64 y) { return x + y; }) + base;
+  if (!summed) {
+    if (r.q > 0 || cx > -INFINITY) part(kept);
+    else part([&](float x, int) { return sample_weight(x, r); });
+    mine = sample_warp_reduce(mine, [](u64 x, u64 y) { return x + y; });
+  } else {
+    mine = base;
+  }
   // the sums of the warps before: of this CTA, then of the cluster
   auto warps = [&](u64 v, u64& block) {
     __syncthreads();

@@ -433,6 +433,30 @@ def test_logits_sample_many_rows(T):
                  top_p=0.3 + 0.8 * torch.rand(1500, generator=g))
 
 
+@pytest.mark.parametrize("m,V,dtype", [(2, 70000, torch.bfloat16), (20, 70000, torch.float32),
+                                       (40, 70000, torch.bfloat16), (150, 40000, torch.float32),
+                                       (150, 40000, torch.bfloat16), (30, 2056, torch.float32)])
+def test_logits_sample_rows_over_clusters(T, m, V, dtype):
+    """Rows in 1 to 8 CTAs of either size; logits so close together that the cut's bin holds a
+    few tokens, hundreds, or more than the list; top_k past what is drawn from a list at once."""
+    n = min(m, 6)                              # distinct rows, taken in turn
+    for i, spread in enumerate((0.05, 0.4, 4.0)):
+        logits, u, g = rows(n, V, spread, 40 + i, dtype)
+        p = torch.rand(n, generator=g)
+        p[0] = 0.0
+        k = torch.randint(0, 1000, (n,), generator=g, dtype=torch.int32)
+        q = 0.9 * torch.rand(n, generator=g)
+        q[::2] = 0.0
+        t = 0.2 + torch.rand(n, generator=g)
+        turn = torch.arange(m) % n
+        for kw in (dict(top_p=p), dict(top_k=k), dict(top_k=k, top_p=p, min_p=q), dict(top_p=p, min_p=q)):
+            kw["temperature"] = t
+            ri, rl = sample_ref(logits, u, **kw)
+            idx, logp = T.logits_sample(logits[turn].cuda(), u[turn].cuda(), **{x: y[turn].cuda() for x, y in kw.items()})
+            assert np.array_equal(idx.cpu().numpy(), ri[turn])
+            assert np.allclose(f64(logp), rl[turn], rtol=2.0 ** -23, atol=1e-6)
+
+
 @pytest.mark.parametrize("m,H,V,tp", [(1, 64, 512, 2), (33, 256, 4096, 8), (70, 128, 1000, 1)])
 def test_vocab_parallel_sample_integer_logits(T, m, H, V, tp):
     """Integer products are exact in fp32, so the drawn token is the oracle's."""
