@@ -28,7 +28,9 @@ torch's own bf16 cast on float32-exact values, hand-picked bf16 ties, and an
 exhaustive property check of the GQA head map; for attention on local heads, the
 closed forms of uniform weights (Q = 0: means and prefix means of V), one key,
 dominant-score selection, torch's own scaled_dot_product_attention (with its
-grouped-query option) and sharded-equals-unsharded for every valid tp. Float
+grouped-query option) and sharded-equals-unsharded for every valid tp; for the
+serving operators (see ``tests/test_serving_host.py``) the limits of a wide window,
+decode steps against the prefill, and cuts and draws by hand. Float
 workloads at full size are
 parity-pinned only through these (no page prints results at those shapes).
 """
