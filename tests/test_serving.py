@@ -643,6 +643,47 @@ def test_decode_workspace_shared_by_calls_of_other_sizes(T):
 
 
 
+def test_two_graphs_share_a_workspace(T):
+    """A windowed and a prefix step, each captured once with the same workspace, replayed in
+    turn with new positions."""
+    hq, hkv, tp, P, cap = 16, 4, 2, 500, 400
+    nkv, cols = geom(hq, hkv, tp)
+    h = T.Heads(hq, hkv, D)
+    pk, pv = WL.gen_normal((nkv, P, D), 1.0, 1111), WL.gen_normal((nkv, P, D), 1.0, 1112)
+    pkg, pvg = pk.cuda(), pv.cuda()
+    ws = T.decode_workspace(9, h, tp, P)
+    sets = []
+    for i, n in enumerate((9, 2)):
+        qkv = WL.gen_normal((n, cols), 1.0, 1113 + i)
+        k, v = caches(n, nkv, cap, 1115 + 2 * i)
+        pos = torch.zeros(n, dtype=torch.int32, device="cuda")
+        x, kg, vg, out = qkv.cuda(), k.cuda(), v.cuda(), torch.empty(n, hq * D, dtype=torch.bfloat16, device="cuda")
+
+        def step(i=i, x=x, pos=pos, kg=kg, vg=vg, out=out):
+            if i:
+                T.sharded_window_decode(x, h, tp, pos, 300, kg, vg, ws, 5, out)
+            else:
+                T.sharded_prefix_decode(x, h, tp, pkg, pvg, pos, kg, vg, ws, out)
+        step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        kg.copy_(k)
+        vg.copy_(v)
+        sets.append((g, qkv, pos, out, f64(k).copy(), f64(v).copy()))
+    for r in range(3):
+        for i, (g, qkv, pos, out, kr, vr) in enumerate(sets):
+            p = [(37 * r + 131 * b) % cap for b in range(qkv.shape[0])]
+            pos.copy_(torch.tensor(p, dtype=torch.int32))
+            g.replay()
+        torch.cuda.synchronize()
+        for i, (g, qkv, pos, out, kr, vr) in enumerate(sets):
+            more = () if i else (f64(pk), f64(pv))
+            close(out, *O.cached_decode(qkv, hq, hkv, D, tp, pos.tolist(), 300 if i else cap, 5 if i else 0, kr, vr, *more))
+
+
+
 @pytest.mark.parametrize("hq", [96, 128, 160])
 def test_decode_many_query_heads_per_kv_head(T, hq):
     h, n, cap, P = T.Heads(hq, 1, D), 3, 70, 150
