@@ -77,8 +77,10 @@ __global__ void __launch_bounds__(kAppendThreads) tps_kv_append_kernel(const KvA
 // block: a place in the workspace that no size moves. It returns to zero.
 // Behind a shared prefix every item leaves a part, to be merged with the prefix kernel's.
 // Merging waits until the CTA's stream has ended and then uses all its warps, one output
-// row each: done where an item ends, it held the stream up (window_decode of 32 sequences
-// with 4100 visible keys: 96 us; 64 sequences behind a prefix of 16384: 118 us).
+// row each: done where an item ends, it held the stream up (64 sequences behind a prefix of
+// 16384 took 118 us with it). Now 32 sequences with windows of 4096 take 92 us (483 MB, 0.80 of
+// the copy rate), one with a window of 2048 12.5 (start 1.3, its block 4, the part 1.5, counting
+// 0.6, the merge of 17 parts 3.5: latencies), 64 behind a prefix 75 in all.
 //
 // Blocks of 128 slots, with the roles of the two products exchanged so that the few heads
 // are the small side: S^T = K Q^T has M = 128 slots, N = 16 heads, K = 128 dimensions;
