@@ -229,7 +229,6 @@ int launch_prefix_attention(const CUtensorMap& tq, const CUtensorMap& tk, const 
                             int grid, cudaStream_t st);
 int launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a, int grid, cudaStream_t st);
 int launch_sample(const SampleArgs& a, int num_sms, cudaStream_t st);   // chooses the slice
-int attention_smem_bytes(int two_tiles);
 // bf16_chain = 0: Y = P_0 + ... + P_{tp-1} (+ bias) in fp32; 1: every P_s rounded to
 // bf16, summed in shard order with a bf16 rounding after each addition, bias added
 // once with one more rounding.

@@ -451,8 +451,6 @@ int launch_argmax_reduce(const void* part, int M, int tp, int per_shard_entries,
   return cudaGetLastError() == cudaSuccess ? 0 : -6;
 }
 
-int attention_smem_bytes(int two_tiles) { return two_tiles ? kAttn2SmemBytes : kAttnSmemBytes; }
-
 // Launches fn in clusters, with its shared-memory opt-in of max_smem bytes (per device,
 // remembered in *attr_done).
 template <class... P, class... Args>

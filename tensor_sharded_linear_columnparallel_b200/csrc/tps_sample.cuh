@@ -42,7 +42,7 @@ namespace tps {
 
 typedef unsigned long long u64;
 
-constexpr int kSampleMaxWarps = 32;
+constexpr int kSampleMaxWarps = 16;
 constexpr int kSampleBins = 1024;
 constexpr int kSampleList = 1024;              // entries of the candidate list, whose second half overlays the histogram
 constexpr u64 kSampleOne = 1ull << 44;         // weight of the largest logit
