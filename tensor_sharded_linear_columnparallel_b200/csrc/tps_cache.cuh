@@ -133,7 +133,7 @@ __device__ __forceinline__ DecView dec_view(const DecodeArgs& a, int t) {
     return v;
   }
   const int R = a.cap - a.nsink;
-  v.ring = min(t - a.nsink + 1, a.window);
+  v.ring = min(t - a.nsink, a.window - 1) + 1;             // no t + 1: pos may be 2^31 - 1
   v.e = (t - a.nsink) % R;
   v.slot = a.nsink + v.e;
   const int first = v.e - (v.ring - 1);                    // ring offset of the oldest, negative when wrapped

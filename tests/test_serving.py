@@ -771,3 +771,28 @@ def test_two_streams_at_once(T):
     for pair in got:
         for (a, i), (b, j) in zip(pair, want):
             assert torch.equal(a, b) and torch.equal(i, j)
+
+
+@pytest.mark.parametrize("nsink", [0, 3])
+def test_window_decode_at_the_last_positions(T, nsink):
+    """Positions up to 2^31 - 1, the largest that an int32 holds."""
+    hq, hkv, tp, cap = 4, 2, 1, 203
+    h, W = T.Heads(hq, hkv, D), cap - nsink - 1
+    nkv, cols = geom(hq, hkv, tp)
+    pos = [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 1 - cap]
+    n = len(pos)
+    qkv = WL.gen_normal((n, cols), 1.0, 1201)
+    k, v = caches(n, nkv, cap, 1202)
+    kg, vg = k.cuda(), v.cuda()
+    out = T.sharded_window_decode(qkv.cuda(), h, tp, torch.tensor(pos, dtype=torch.int32, device="cuda"), W, kg, vg,
+                                  T.decode_workspace(n, h, tp), nsink=nsink)
+    kr, vr = f64(k).copy(), f64(v).copy()
+    O.kv_append(qkv, hq, hkv, D, tp, n, 1, pos, [1] * n, nsink, kr, vr)
+    assert np.array_equal(f64(kg), kr) and np.array_equal(f64(vg), vr)
+    q = f64(qkv)
+    for b, t in enumerate(pos):
+        slots = [O.cache_slot(j, nsink, cap) for j in [*range(nsink), *range(t - W + 1, t + 1)]]
+        for hd in range(hq):
+            g = hd // (hq // hkv)
+            ref, mag = O.attend(q[b, hd * D:(hd + 1) * D], kr[b, g, slots], vr[b, g, slots])
+            close(out[b, hd * D:(hd + 1) * D], ref, mag, f"position {t}")
