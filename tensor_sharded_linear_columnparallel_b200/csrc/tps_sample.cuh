@@ -48,6 +48,7 @@ constexpr int kSampleList = 1024;              // entries of the candidate list,
 constexpr u64 kSampleOne = 1ull << 44;         // weight of the largest logit
 constexpr int kSampleFew = 64;                 // entries that sample_select compares with one another
 constexpr int kSampleSmall = 256;              // kept tokens that the first CTA draws from by itself
+constexpr float kSampleSpan = 46.2f;           // 32 log2(e): logits this many factors of 2 below the largest have no weight
 
 __device__ __forceinline__ void atomic_add_cluster_u64(uint32_t addr, u64 x) {
   asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;" ::"r"(addr), "l"(x) : "memory");
@@ -383,14 +384,28 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
     mx = fmaxf(mx, s.fred[w]);
     mn = fminf(mn, s.fred[WARPS + w]);
   }
-  if (mn == -INFINITY && mx > -INFINITY) {     // masked logits: the smallest of the others
+  // The bins divide the range of the logits that have a weight. Masks (-inf, the type's lowest
+  // value, -1e4) and outliers of that size become -inf and leave it: stretched by them, a cut's bin
+  // outgrows the list (8 rows of 128256, top_p 0.9, the last 20000 masked: 527 us, so 25; top_k 50,
+  // all but 30 masked by the lowest value: 264 and 15). No logits of a model's own lie 1024 below its largest.
+  auto weightless = [&](float top, float x) { return (top - x) * cf > kSampleSpan; };
+  auto masked = [&](float top, float low) {
+    return __builtin_expect(top - low > 1024.0f && weightless(top, low), false);
+  };
+  const float own = mx;                        // this CTA's largest
+  if (!greedy && mx > -INFINITY && mx < INFINITY && masked(mx, mn)) {
     mn = INFINITY;
     for (int v = tid; v < n / 4; v += THREADS) {
       float x[4];
       sample_get4(xs, v, x);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) mn = x[j] > -INFINITY ? fminf(mn, x[j]) : mn;
+      for (int j = 0; j < 4; ++j) {
+        if (weightless(own, x[j])) x[j] = -INFINITY;
+        else mn = fminf(mn, x[j]);
+      }
+      sample_put4(xs, v, x);
     }
+    if (weightless(own, most)) most = -INFINITY;
     mn = sample_warp_reduce(mn, [](float x, float y) { return fminf(x, y); });
     __syncthreads();
     if (lane == 0) s.fred[warp] = mn;
@@ -407,10 +422,23 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
   }
   cluster_sync_all();
   u64 have = 0;
+  auto top_of = [&](int r) { return __uint_as_float(static_cast<uint32_t>(s.top[r] >> 32)); };
+  auto low_of = [&](int r) { return __uint_as_float(static_cast<uint32_t>(s.top[r])); };
   for (int r = 0; r < cs; ++r) {
     have += s.have[r];
-    mx = fmaxf(mx, __uint_as_float(static_cast<uint32_t>(s.top[r] >> 32)));
-    mn = fminf(mn, __uint_as_float(static_cast<uint32_t>(s.top[r])));
+    mx = fmaxf(mx, top_of(r));
+    mn = fminf(mn, low_of(r));
+  }
+  bool hidden = false;                         // none of this CTA's tokens has a weight
+  if (masked(mx, mn)) {                        // leaves out such CTAs
+    have = 0;
+    mn = INFINITY;
+    for (int r = 0; r < cs; ++r)
+      if (!weightless(mx, top_of(r))) {
+        have += s.have[r];
+        mn = fminf(mn, low_of(r));
+      }
+    hidden = weightless(mx, own);
   }
 
   float cx = -INFINITY;                        // kept: x > cx, or x == cx and index <= ci (and min_p)
@@ -456,11 +484,15 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
     most = -INFINITY;
     have = 0;                                  // top_k counts tokens
     __syncthreads();
+  } else if (__builtin_expect(hidden, false)) {
+    for (int v = tid; v < n / 4; v += THREADS) sample_put4(xs, v, {-INFINITY, -INFINITY, -INFINITY, -INFINITY});
+    most = -INFINITY;
+    __syncthreads();
   }
   r.mxf = mx;
   r.mx = static_cast<double>(mx);
   // 2^octave bins per factor of 2 in the weight: as many as keep the range within the bins
-  const float span = fminf((mx - mn) * cf, 46.2f);    // in factors of 2; 46.2 = 32 log2(e)
+  const float span = fminf((mx - mn) * cf, kSampleSpan);   // in factors of 2
   const int octave = span > 0.0f ? min(100, ilogbf(static_cast<float>(kSampleBins - 1) / span)) : 0;   // at least 4
   r.bin_scale = scalbnf(cf, octave);
   r.octave = min(octave, 31);

@@ -796,3 +796,115 @@ def test_window_decode_at_the_last_positions(T, nsink):
             g = hd // (hq // hkv)
             ref, mag = O.attend(q[b, hd * D:(hd + 1) * D], kr[b, g, slots], vr[b, g, slots])
             close(out[b, hd * D:(hd + 1) * D], ref, mag, f"position {t}")
+
+
+# ============================================================ masks over clusters
+def sample_by_numpy(logits, u, temperature, top_k, top_p, min_p):
+    """sample_row with numpy's sorts and sums, for long rows."""
+    l = f64(logits)
+    l[np.isnan(l)] = -np.inf
+    mx = l.max()
+    if mx == -np.inf:
+        return -1, -np.inf
+    w = np.where(l == mx, 1.0, 0.0) if mx == np.inf else np.exp((l - mx) / temperature)
+    order = np.lexsort((np.arange(len(l)), -l))[:top_k or len(l)]
+    if top_p < 1:
+        c = np.cumsum(w[order])
+        order = order[np.concatenate([[0.0], c[:-1]]) < top_p * c[-1]]
+    kept = np.sort(order)
+    kept = kept[(w[kept] >= min_p) & (w[kept] > 0)]
+    c = np.cumsum(w[kept])
+    i = min(np.searchsorted(c, u * c[-1], side="right"), len(kept) - 1)
+    return kept[i], math.log(w[kept[i]] / c[-1])
+
+
+MASKS = {  # part of a row of V logits that is hidden, by token
+    "tail": lambda i, V: i >= V - V * 5 // 32,
+    "head": lambda i, V: i < V // 3,
+    "all but the last few": lambda i, V: i < V - 11,
+    "all but one": lambda i, V: i != V // 2 + 5,
+    "middle and scattered": lambda i, V: ((i > V // 8) & (i < V // 2)) | (i % 3 == 0),
+    "all": lambda i, V: i >= 0,
+}
+
+
+@pytest.mark.parametrize("m,V,dtype", [(6, 40000, torch.float32), (6, 128256, torch.bfloat16),
+                                       (64, 128256, torch.bfloat16), (200, 70000, torch.float32)])
+@pytest.mark.parametrize("hide", ["-inf", "nan", "lowest", "-1e4"])
+def test_logits_sample_masks_over_clusters(T, m, V, dtype, hide):
+    """Whole parts of the CTAs of a cluster hidden: by -inf, NaN, the type's lowest value, or -1e4.
+    top_k is larger than what some masks leave."""
+    value = {"-inf": -math.inf, "nan": math.nan, "lowest": torch.finfo(dtype).min, "-1e4": -1e4}[hide]
+    logits, u, g = rows(len(MASKS), V, 1.5, 61, dtype)
+    for r, mask in enumerate(MASKS.values()):
+        logits[r, mask(torch.arange(V), V)] = value
+    if math.isfinite(value):
+        logits[-1, 0] = 0.0                    # a row of equal lowest values has weights; here all but one have none
+    turn = torch.arange(m) % len(MASKS)
+    none = dict(temperature=0.7, top_k=0, top_p=1.0, min_p=0.0)
+    for kw in ({}, dict(top_k=50), dict(top_p=0.9), dict(min_p=0.05), dict(top_k=3000, top_p=0.8), dict(top_k=9, min_p=0.2)):
+        par = {**none, **kw}
+        ref = [sample_by_numpy(logits[i], float(u[i]), *(float(np.float32(par[x])) if x != "top_k" else par[x] for x in none))
+               for i in range(len(MASKS))]
+        idx, logp = T.logits_sample(logits[turn].cuda(), u[turn].cuda(), **{
+            x: torch.full((m,), y, dtype=torch.int32 if x == "top_k" else torch.float32, device="cuda") for x, y in par.items()})
+        ri, rl = np.array([x[0] for x in ref])[turn], np.array([x[1] for x in ref])[turn]
+        assert np.array_equal(idx.cpu().numpy(), ri), (kw, idx.tolist()[:6], ri.tolist()[:6])
+        fin = np.isfinite(rl)
+        assert np.allclose(f64(logp)[fin], rl[fin], rtol=2.0 ** -23, atol=1e-6)
+        assert np.array_equal(f64(logp)[~fin], rl[~fin])
+
+
+@pytest.mark.parametrize("m,V", [(6, 40000), (64, 128256)])
+def test_logits_sample_infinities_over_clusters(T, m, V):
+    """+inf in one CTA only, or in two, beside finite logits, -inf and NaN; top_k of one token, and
+    of more than the others."""
+    logits, u, g = rows(6, V, 1.5, 62)
+    logits[0, V - 3] = math.inf
+    logits[1, [5, V - 5]] = math.inf
+    logits[2, :V // 2] = -math.inf
+    logits[2, 1::2] = math.nan
+    logits[3, V // 3] = math.inf
+    logits[3, V // 2:] = -math.inf
+    logits[4, 100:] = math.nan
+    logits[4, :90] = -math.inf
+    turn = torch.arange(m) % 6
+    for k, p, q in ((0, 1.0, 0.0), (1, 1.0, 0.0), (V // 2 + 7, 1.0, 0.0), (0, 0.6, 0.0), (0, 1.0, 0.3), (40, 0.9, 0.01)):
+        ref = [sample_by_numpy(logits[i], float(u[i]), 1.0, k, float(np.float32(p)), float(np.float32(q))) for i in range(6)]
+        full = lambda x, t=torch.float32: torch.full((m,), x, dtype=t, device="cuda")
+        idx, logp = T.logits_sample(logits[turn].cuda(), u[turn].cuda(), top_k=full(k, torch.int32), top_p=full(p), min_p=full(q))
+        assert np.array_equal(idx.cpu().numpy(), np.array([x[0] for x in ref])[turn]), (k, p, q)
+        assert np.allclose(f64(logp), np.array([x[1] for x in ref])[turn], rtol=2.0 ** -23, atol=1e-6)
+
+
+@pytest.mark.parametrize("hide", [-math.inf, torch.finfo(torch.float32).min, -1e4])
+@pytest.mark.parametrize("top_k,top_p", [(0, 0.9), (50, 1.0)])
+def test_logits_sample_masked_rows_are_as_fast(T, hide, top_k, top_p):
+    """A masked tail, or a mask that leaves 30 tokens, costs no more than three times the whole row:
+    the cut is found from the bins and the list. Bit by bit it takes 64 passes over the row."""
+    m, V = 8, 128256
+    full = lambda x, t=torch.float32: torch.full((m,), x, dtype=t, device="cuda")
+    kw = dict(top_k=full(top_k, torch.int32), top_p=full(top_p))
+    logits, u, _ = rows(m, V, 0.5, 63)
+    tail, few = logits.clone(), logits.clone()
+    tail[:, V - 20000:] = hide
+    few[:, 30:] = hide
+    u = u.cuda()
+
+    def time_us(l):
+        l = l.cuda()
+        best = math.inf
+        for _ in range(8):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda._sleep(400_000)         # the calls are issued meanwhile
+            a.record()
+            for _ in range(10):
+                T.logits_sample(l, u, **kw)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b) * 100)
+        return best
+    whole = time_us(logits)
+    times = [time_us(tail), time_us(few)]
+    print(f"\nwhole {whole:.1f} us, masked tail {times[0]:.1f} us, 30 tokens {times[1]:.1f} us")
+    assert max(times) <= 3 * whole, (whole, times)
