@@ -379,8 +379,9 @@ TPS_API int sharded_kv_append(const void* qkv, int64_t nseq, int64_t seqlen, con
  *   unused slot of the batch: its caches stay as they are and its output is zero.
  *   ws: device workspace of at least tps_decode_workspace_bytes(nseq, heads, tp, 0)
  *   bytes, zero-filled before its first use and left ready for the next call of either
- *   kind and any size; calls that share one are ordered by their stream. The positions are read on the device:
- *   a captured graph replays with the positions of its replay.
+ *   kind; calls that share one are ordered by their stream. The positions are read on
+ *   the device while the call runs: a captured graph replays with the positions of its
+ *   replay.
  *   Softmax in fp32, weights rounded to bf16 for the product with V (fp32 accumulation).
  *   Errors as sharded_kv_append, and TPS_ERR_WORKSPACE.
  */
@@ -396,14 +397,20 @@ TPS_API int sharded_window_decode(const void* qkv, int64_t nseq, const tps_heads
  *   when prefix_len = 0; at most 128 query heads per KV head of a shard otherwise,
  *   TPS_ERR_UNIMPLEMENTED). pos[b] counts the tokens behind the prefix; a row with pos[b]
  *   outside [0, cap) is unused as above. ws: at least
- *   tps_decode_workspace_bytes(nseq, heads, tp, prefix_len) bytes.
+ *   tps_decode_workspace_bytes(nseq, heads, tp, prefix_len) bytes. In a smaller one the
+ *   prefix is read in fewer parts, as many as fit; TPS_ERR_WORKSPACE when not even one does.
  */
 TPS_API int sharded_prefix_decode(const void* qkv, int64_t nseq, const tps_heads* heads, int tp,
                                   const void* prefix_k, const void* prefix_v, int64_t prefix_len,
                                   const int32_t* pos, void* k_cache, void* v_cache, int64_t cap, void* attn_out,
                                   void* ws, size_t ws_bytes, void* stream);
 
-/* tps_decode_workspace_bytes -- workspace of the two decode calls; 0 for invalid arguments. */
+/*
+ * tps_decode_workspace_bytes -- workspace of the two decode calls; 0 for invalid
+ *   arguments. It serves every call with the same heads and tp of up to nseq sequences,
+ *   without a prefix or behind one of any length; prefixes of up to prefix_len tokens are
+ *   read in as many parts as suit them best.
+ */
 TPS_API size_t tps_decode_workspace_bytes(int64_t nseq, const tps_heads* heads, int tp, int64_t prefix_len);
 
 /*

@@ -1177,6 +1177,23 @@ int cache_geom(const tps_heads* heads, int tp, int64_t nsink, int64_t cap, HeadM
   return TPS_OK;
 }
 
+// Parts into which a prefix kernel cuts the key blocks of a KV head slot, at most `most`: the
+// fewest block times on the critical path, a part costing about three blocks more than its own
+// (start, output, merge). pairs: (KV head slot, pair of tiles).
+int prefix_splits(int64_t pairs, int nkb, int sms, int64_t most) {
+  int splits = 1;
+  int64_t best = -1;
+  for (int n = 1; n <= nkb && n <= sms && n <= most; ++n) {
+    const int64_t waves = (pairs * n + sms - 1) / sms;
+    const int64_t cost = waves * ((nkb + n - 1) / n + 3);
+    if (best < 0 || cost < best) {
+      best = cost;
+      splits = n;
+    }
+  }
+  return splits;
+}
+
 // Workspace of a decode step: header, a counter per CTA, the decode kernel's parts, then the
 // prefix kernel's max / sum and parts.
 struct DecodeWs {
@@ -1184,8 +1201,11 @@ struct DecodeWs {
   int bpt, tiles, splits, nkb;  // prefix kernel: sequences per tile, tiles, parts of the key blocks
   size_t counters, parts, item_parts, ml, prefix_parts, bytes;
 };
+constexpr size_t kPrefixPartBytes = (256 + 128 * 128) * 4;   // max and sum, output
 
-DecodeWs decode_ws(int64_t nseq, const HeadMap& hm, int64_t nkv, int64_t prefix_len, int sms) {
+// The layout for a call given ws_bytes: where the prefix parts that suit it best do not fit, as
+// many as do (never fewer than one per tile, whether or not that fits).
+DecodeWs decode_ws(int64_t nseq, const HeadMap& hm, int64_t nkv, int64_t prefix_len, int sms, size_t ws_bytes) {
   DecodeWs w{};
   const int G = hm.qs / hm.kvs;
   w.nch = (G + 15) / 16;
@@ -1198,28 +1218,34 @@ DecodeWs decode_ws(int64_t nseq, const HeadMap& hm, int64_t nkv, int64_t prefix_
     w.bpt = 128 / G;
     w.tiles = static_cast<int>((nseq + w.bpt - 1) / w.bpt);
     w.nkb = static_cast<int>((prefix_len + 127) / 128);
-    // Parts of the key blocks: the fewest block times on the critical path, a part costing
-    // about three blocks more than its own (start, output, merge).
-    const int64_t pairs = nkv * ((w.tiles + 1) / 2);
-    int64_t best = -1;
-    for (int n = 1; n <= std::min(w.nkb, sms); ++n) {
-      const int64_t waves = (pairs * n + sms - 1) / sms;
-      const int64_t cost = waves * ((w.nkb + n - 1) / n + 3);
-      if (best < 0 || cost < best) {
-        best = cost;
-        w.splits = n;
-      }
-    }
-    const size_t np = static_cast<size_t>(nkv) * w.tiles * w.splits;
     w.item_parts = at;
     at += round256(static_cast<size_t>(nseq) * nkv * w.nch * tps::kDecPartFloats * 4);
     w.ml = at;
-    at += np * 256 * 4;
-    w.prefix_parts = at;
-    at += np * 128 * 128 * 4;
+    const size_t per = static_cast<size_t>(nkv) * w.tiles;   // parts of one split
+    const size_t fit = ws_bytes > at && per > 0 ? (ws_bytes - at) / (per * kPrefixPartBytes) : 1;
+    w.splits = prefix_splits(nkv * ((w.tiles + 1) / 2), w.nkb, sms, static_cast<int64_t>(std::min<size_t>(fit, 1u << 30)));
+    w.prefix_parts = at + per * w.splits * 256 * 4;
+    at += per * w.splits * kPrefixPartBytes;
   }
   w.bytes = at;
   return w;
+}
+
+// What a workspace has to hold so that up to nseq sequences behind up to prefix_len tokens get the
+// parts that suit them best. Their number is no monotone function of the sizes (64 sequences behind 16384
+// tokens, 32 / 8 heads, take 16 parts per tile, 65 sequences 9), so it is the most that any fewer
+// tiles take: behind the same prefix, or, in one wave of CTAs, behind a shorter one. (Rarer
+// plans, in several waves behind a shorter prefix or for over 1024 tiles less, get what fits.)
+size_t decode_ws_bound(int64_t nseq, const HeadMap& hm, int64_t nkv, int64_t prefix_len, int sms) {
+  const DecodeWs w = decode_ws(nseq, hm, nkv, prefix_len, sms, SIZE_MAX);
+  if (w.tiles == 0) return w.bytes;
+  int64_t most = 0;
+  for (int64_t t = std::max(1, w.tiles - 1023); t <= w.tiles; ++t) {
+    const int64_t pairs = nkv * ((t + 1) / 2);
+    const int64_t wave = std::min<int64_t>(w.nkb, sms / pairs);
+    most = std::max(most, t * std::max<int64_t>(prefix_splits(pairs, w.nkb, sms, w.nkb), wave));
+  }
+  return w.ml + static_cast<size_t>(nkv * most) * kPrefixPartBytes;
 }
 
 // One decode step; *a carries the mask.
@@ -1241,7 +1267,7 @@ int run_decode(const void* qkv, int64_t nseq, const tps_heads* heads, const Head
   const int64_t blocks = nseq * nkv * ((hm.qs / hm.kvs + 15) / 16) * (room + (cap + 127) / 128);   // places, at most
   if (blocks > 0x7fffffffLL) return TPS_ERR_ARG;
   const int sms = num_sms_current();
-  const DecodeWs lay = decode_ws(nseq, hm, nkv, prefix_len, sms);
+  const DecodeWs lay = decode_ws(nseq, hm, nkv, prefix_len, sms, ws_bytes);
   if (ws_bytes < lay.bytes) return TPS_ERR_WORKSPACE;
   int rc = check_device();
   if (rc) return rc;
@@ -1718,7 +1744,7 @@ size_t tps_decode_workspace_bytes(int64_t nseq, const tps_heads* heads, int tp, 
   if (nseq < 0 || nseq > (1LL << 24) || prefix_len < 0 || prefix_len > (1LL << 30) ||
       cache_geom(heads, tp, 0, 1, &hm) != TPS_OK)
     return 0;
-  return decode_ws(nseq, hm, static_cast<int64_t>(tp) * hm.kvs, prefix_len, num_sms_current()).bytes;
+  return decode_ws_bound(nseq, hm, static_cast<int64_t>(tp) * hm.kvs, prefix_len, num_sms_current());
 }
 
 int sharded_window_decode(const void* qkv, int64_t nseq, const tps_heads* heads, int tp, const int32_t* pos,

@@ -908,3 +908,29 @@ def test_logits_sample_masked_rows_are_as_fast(T, hide, top_k, top_p):
     times = [time_us(tail), time_us(few)]
     print(f"\nwhole {whole:.1f} us, masked tail {times[0]:.1f} us, 30 tokens {times[1]:.1f} us")
     assert max(times) <= 3 * whole, (whole, times)
+
+
+def test_decode_workspace_serves_smaller_batches(T):
+    """A workspace made for the largest batch serves it when rows leave, and other prefixes: the
+    same bits as a workspace of the call's own. One made for a shorter prefix gives fewer parts."""
+    hq, hkv, tp, P, cap = 32, 8, 8, 16384, 20
+    nkv, cols = geom(hq, hkv, tp)
+    h = T.Heads(hq, hkv, D)
+    pk, pv = WL.gen_normal((nkv, P, D), 1.0, 1211), WL.gen_normal((nkv, P, D), 1.0, 1212)
+    qkv, (k, v) = WL.gen_normal((65, cols), 1.0, 1213), caches(65, nkv, cap, 1214)
+    shared, least = T.decode_workspace(65, h, tp, P), T.decode_workspace(65, h, tp, 1)
+    for n, prefix in ((65, P), (64, P), (33, P), (32, P), (1, P), (64, 2304), (8, 2304), (65, 0), (1, 1)):
+        x, kg, vg = qkv[:n].cuda(), k[:n].cuda().contiguous(), v[:n].cuda().contiguous()
+        pos = torch.arange(n, dtype=torch.int32, device="cuda") % cap
+        args = (pk[:, :prefix].cuda().contiguous(), pv[:, :prefix].cuda().contiguous()) if prefix else (None, None)
+        call = lambda ws: T.sharded_prefix_decode(x, h, tp, *args, pos, kg, vg, ws)
+        got = call(shared)
+        assert torch.equal(got, call(T.decode_workspace(n, h, tp, prefix))), (n, prefix)
+        if n == 33:
+            ref, mag = O.cached_decode(qkv[:n], hq, hkv, D, tp, pos.tolist(), cap, 0, f64(k[:n]).copy(), f64(v[:n]).copy(),
+                                       f64(pk), f64(pv))
+            close(got, ref, mag)
+            close(call(least), ref, mag)
+    with pytest.raises(T.TpsError) as e:
+        call(T.decode_workspace(1, h, tp))
+    assert e.value.status == T.TPS_ERR_WORKSPACE

@@ -210,3 +210,14 @@ def test_sampling_checks(T):
     assert vps(nb=256) == T.TPS_ERR_WORKSPACE
     assert vps(m=-1) == T.TPS_ERR_ARG
     assert vps(m=0, X=None, ws=None, nb=0) == T.TPS_OK
+
+
+@pytest.mark.parametrize("hq,hkv,tp", [(32, 8, 8), (32, 8, 4), (64, 8, 8), (28, 4, 2), (16, 1, 4), (32, 32, 4), (4, 1, 1)])
+def test_decode_workspace_grows_with_its_sizes(T, hq, hkv, tp):
+    """A workspace for a batch behind a prefix is large enough for fewer sequences and shorter prefixes."""
+    h = heads(T, hq, hkv)
+    lens = (0, 1, 128, 1000, 2304, 5000, 16384, 100000)
+    need = np.array([[T.lib.tps_decode_workspace_bytes(n, h, tp, P) for P in lens] for n in range(0, 260)], dtype=np.int64)
+    assert (need > 0).all()
+    assert (np.diff(need, axis=0) >= 0).all(), np.argwhere(np.diff(need, axis=0) < 0)[:5]
+    assert (np.diff(need, axis=1) >= 0).all(), np.argwhere(np.diff(need, axis=1) < 0)[:5]
