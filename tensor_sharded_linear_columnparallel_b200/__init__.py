@@ -559,8 +559,10 @@ def sharded_prefix_decode(qkv: torch.Tensor, heads: Heads, tp: int, prefix_k, pr
     pk, pv, cap = _cache_args(k_cache, v_cache, nseq, nkv, heads.head_dim, dev)
     P, fk, fv = 0, None, None
     if prefix_k is not None or prefix_v is not None:
-        P = _need(prefix_k, "prefix_k").shape[1] if prefix_k.dim() == 3 else -1
-        fk = _arg(prefix_k, "prefix_k", torch.bfloat16, (nkv, P, heads.head_dim), dev)
+        fk = _arg(_need(prefix_k, "prefix_k"), "prefix_k", torch.bfloat16, None, dev)
+        if prefix_k.dim() != 3 or prefix_k.shape[0] != nkv or prefix_k.shape[2] != heads.head_dim:
+            raise ValueError(f"prefix_k must have shape ({nkv}, prefix_len, {heads.head_dim}), got {tuple(prefix_k.shape)}")
+        P = prefix_k.shape[1]
         fv = _arg(_need(prefix_v, "prefix_v"), "prefix_v", torch.bfloat16, (nkv, P, heads.head_dim), dev)
     pp = _arg(_need(pos, "pos"), "pos", torch.int32, (nseq,), dev)
     pw = _arg(_need(ws, "ws"), "ws", None, None, dev)

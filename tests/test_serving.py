@@ -934,3 +934,17 @@ def test_decode_workspace_serves_smaller_batches(T):
     with pytest.raises(T.TpsError) as e:
         call(T.decode_workspace(1, h, tp))
     assert e.value.status == T.TPS_ERR_WORKSPACE
+
+
+def test_prefix_decode_refuses_half_a_prefix(T):
+    h = T.Heads(4, 2, D)
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device="cuda")
+    call = lambda pk, pv: T.sharded_prefix_decode(z(2, geom(4, 2, 2)[1]), h, 2, pk, pv, z(2, dtype=torch.int32), z(2, 2, 8, D),
+                                                  z(2, 2, 8, D), T.decode_workspace(2, h, 2, 5))
+    with pytest.raises(TypeError):
+        call(None, z(2, 5, D))
+    with pytest.raises(TypeError):
+        call(z(2, 5, D), None)
+    for pk in (z(5, D), z(1, 5, D), z(2, 5, 64), z(2, 10, D)[:, ::2]):
+        with pytest.raises(ValueError):
+            call(pk, z(2, 5, D))
