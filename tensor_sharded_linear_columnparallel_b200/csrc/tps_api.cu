@@ -1314,7 +1314,6 @@ int run_decode(const void* qkv, int64_t nseq, const tps_heads* heads, const Head
     p.status = a->status;
     p.parts = reinterpret_cast<float*>(wsp + lay.prefix_parts);
     p.ml = reinterpret_cast<float*>(wsp + lay.ml);
-    p.nkv = a->nkv;
     p.bpt = lay.bpt;
     p.tiles = lay.tiles;
     p.splits = lay.splits;

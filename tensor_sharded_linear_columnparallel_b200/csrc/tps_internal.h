@@ -105,7 +105,7 @@ struct AttnArgs {
   // parts[p][128 * 128] (unnormalised output, an image of attn_part_index), ml[p][2][128]
   // (reference max in log2 units, sum).
   float *parts, *ml;
-  int nkv, bpt, tiles, splits;
+  int bpt, tiles, splits;
 };
 
 // One append of a QKV output's K and V to the shards' caches (tps_cache.cuh).
