@@ -219,7 +219,7 @@ def tps_debug_wait_timeout(timeout_us: int, ws: torch.Tensor | None = None, stre
 def workspace(fn: int, m: int, n: int, k: int, tp: int, device=None) -> torch.Tensor:
     """Zero-filled workspace buffer of tps_workspace_bytes(...) bytes."""
     nbytes = tps_workspace_bytes(fn, m, n, k, tp)
-    return torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(max(nbytes, 16), dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 # ---------------------------------------------------------------- entry points
@@ -513,7 +513,7 @@ def tps_decode_workspace_bytes(nseq: int, heads: Heads, tp: int, prefix_len: int
 
 def decode_workspace(nseq: int, heads: Heads, tp: int, prefix_len: int = 0, device=None) -> torch.Tensor:
     """Zero-filled workspace of the decode calls (tps_decode_workspace_bytes bytes)."""
-    dev = torch.device(device or "cuda")
+    dev = torch.device("cuda" if device is None else device)
     with torch.cuda.device(dev):
         nbytes = tps_decode_workspace_bytes(nseq, heads, tp, prefix_len)
     if nbytes == 0:

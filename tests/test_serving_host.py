@@ -221,3 +221,16 @@ def test_decode_workspace_grows_with_its_sizes(T, hq, hkv, tp):
     assert (need > 0).all()
     assert (np.diff(need, axis=0) >= 0).all(), np.argwhere(np.diff(need, axis=0) < 0)[:5]
     assert (np.diff(need, axis=1) >= 0).all(), np.argwhere(np.diff(need, axis=1) < 0)[:5]
+
+
+def test_workspaces_on_a_device_given_by_number(T, monkeypatch):
+    """Device 0 is the first GPU, not the current one."""
+    import contextlib
+    seen = []
+    monkeypatch.setattr(T.torch, "zeros", lambda *a, device, **k: seen.append(T.torch.device(device)))
+    monkeypatch.setattr(T.torch.cuda, "device", lambda d: contextlib.nullcontext())
+    for given, want in ((0, "cuda:0"), (1, "cuda:1"), ("cuda:1", "cuda:1"), (None, "cuda")):
+        T.workspace(T.FN_SAMPLE, 1, 64, 64, 1, device=given)
+        T.decode_workspace(1, T.Heads(4, 2, 128), 1, device=given)
+        assert [str(d) for d in seen] == [want] * 2
+        seen.clear()
