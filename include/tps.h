@@ -435,7 +435,9 @@ TPS_API size_t tps_decode_workspace_bytes(int64_t nseq, const tps_heads* heads, 
  *   their value (relative) and half a unit; sums of them are exact, so a result depends
  *   neither on the order of the additions nor on the launch.
  *   out_logp: device fp32 [m] or NULL. V must be a multiple of 8 (TPS_ERR_ALIGN) and at
- *   most 393216 (TPS_ERR_UNIMPLEMENTED). Errors: TPS_ERR_ARG, TPS_ERR_DTYPE,
+ *   most 393216 (TPS_ERR_UNIMPLEMENTED). A row with over 1024 logits too close to a cut to
+ *   be told apart at first (many equal ones, or a vocabulary of 200000 and more cut to
+ *   top_p) gives the same result in some 20 to 40 times the time. Errors: TPS_ERR_ARG, TPS_ERR_DTYPE,
  *   TPS_ERR_ALIGN, TPS_ERR_DEVICE, TPS_ERR_CUDA.
  */
 TPS_API int logits_sample(const void* logits, int logits_dtype, int64_t m, int64_t V, const float* u,

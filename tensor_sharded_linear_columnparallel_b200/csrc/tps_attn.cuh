@@ -18,6 +18,11 @@
 // landed. The row sum of the weights, kept against the same reference, divides O
 // at the end -- the result is the same softmax, whatever the reference.
 //
+// P is rounded to bf16 because the product takes both operands in one 16-bit type and V is
+// bf16 (the sum of the weights stays fp32). Over normal inputs that leaves the output 1.35
+// times as far from 64 bits as one rounding of the output alone (relative Frobenius error 0.0022-0.0023
+// against 0.00166, for 300 to 16384 visible keys).
+//
 // Roles (11 warps): 0 = Q and K loads, 1 = MMA issue, 2 = V loads, 3..10 =
 // softmax and output, two warps per query row: warps w and w+4 read the same
 // tensor-memory lanes and take 64 of the 128 keys of each block (and 64 of the

@@ -93,8 +93,9 @@ __global__ void __launch_bounds__(kAppendThreads) tps_kv_append_kernel(const KvA
 //    the token does not see are zeroed there too: a slot never written may hold a NaN.
 //  - The reference max behind P moves only when a score exceeds it by more than 8 (base 2):
 //    one vote per block, and a reduction over the block only then (always at an item's
-//    first block). The weights are rounded to bf16 for the product, as in the prefill; the
-//    sum keeps them in fp32, a partial sum per thread until the item ends.
+//    first block). The weights are rounded to bf16 for the product, as in the prefill (the
+//    reason and the price stand there); the sum keeps them in fp32, a partial sum per thread
+//    until the item ends.
 constexpr int kDecWarps = 12;                                     // warps 7-11 only merge; more would leave each 128 registers
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kDecStages = 3;

@@ -2,10 +2,10 @@
 // temperature, then top-k, then top-p over what is left, then min-p, then the inverse
 // of the running sum of the kept weights in vocabulary order.
 //
-// w_i = exp((l_i - max) / T) as an integer in units of 2^-44. Sums of integers are exact
-// and do not depend on the order of the additions, and they agree with 64-bit floating
-// point to half a unit per token; a float sum would let the rounding of a sum over
-// 128256 tokens decide which token a uniform number falls on.
+// w_i = exp((l_i - max) / T) as an integer in units of 2^-44, within 2^-36 of itself and half
+// a unit. Sums of integers are exact and do not depend on the order of the additions; a float
+// sum would let the rounding of a sum over 128256 tokens decide which token a uniform number
+// falls on.
 //
 // Every filter keeps a top part of the order (logit descending, index ascending), so a
 // row's filters are one threshold, the last kept token, and no sort of the row is needed.
@@ -24,8 +24,11 @@
 // by comparing itself with the others, without a sort. After a cut to p it sends the weights
 // of the list's kept tokens to the warps whose tokens they are, so that the draw needs no pass
 // over the row. Bins are equal parts of the logits within 32 T of the maximum (what lies below
-// has no weight). Where they hold more than the list (equal logits, one far outlier that
-// stretches them), the threshold is found bit by bit from passes over shared memory.
+// has no weight). Where the cut's bin holds more than the list of 1024, the threshold is found
+// bit by bit from 64 passes over shared memory: with many equal logits, an outlier that stretches
+// the bins (masks do not, see there), and in large vocabularies, whose bins hold more. Normal
+// logits cut to p: never at 151936, some rows at 202048, most from 262144 on, where 8 rows then
+// take 980 us instead of 34.
 //
 // Bound by latency for few rows: of the 46,000 cycles of one of 8 rows of 128256 bf16 logits cut
 // to p (512 threads, eight CTAs), 4,000 load it, 7,600 fill the histogram, 3,700 find the bin,
@@ -386,8 +389,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) tps_sample_kernel(const SampleA
   }
   // The bins divide the range of the logits that have a weight. Masks (-inf, the type's lowest
   // value, -1e4) and outliers of that size become -inf and leave it: stretched by them, a cut's bin
-  // outgrows the list (8 rows of 128256, top_p 0.9, the last 20000 masked: 527 us, so 25; top_k 50,
-  // all but 30 masked by the lowest value: 264 and 15). No logits of a model's own lie 1024 below its largest.
+  // outgrows the list (8 rows of 128256, top_p 0.9, the last 20000 masked: 527 us, so 26; top_k 50,
+  // all but 30 masked by the lowest value: 264 and 16). No logits of a model's own lie 1024 below its largest.
   auto weightless = [&](float top, float x) { return (top - x) * cf > kSampleSpan; };
   auto masked = [&](float top, float low) {
     return __builtin_expect(top - low > 1024.0f && weightless(top, low), false);
